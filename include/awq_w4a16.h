@@ -373,6 +373,95 @@ int w4a16_gemv_max_m(int N, int K);
 /* Workspace bytes a call needs on the current device (0 if none); SIZE_MAX for invalid sizes. */
 size_t w4a16_workspace_bytes(int mode, int M, int N, int K, int g);
 
+/* ---------------------------------------------------------------------------------------------------
+ * 8-BIT BLOCK-SCALED OPERATORS
+ *
+ * The pages' frameworks offer 8-bit kernels beside the 4-bit ones ([LLM-AWQ]: the w8a8 kernel folder); the format here is
+ * the library's own.  An 8-bit matrix X [R][K] is two arrays:
+ *   codes   uint8_t[R][K], row major: e4m3 (4 exponent bits, 3 mantissa bits, largest value 448).
+ *   scales  uint8_t[R][SC], SC = ceil(K / 128) rounded up to a multiple of 4: byte b of row r, block j (columns 128 j ..)
+ *           stands for 2^(b - 127) (e8m0); the bytes past the last block are 127 and are not read.
+ * The value of column k of row r is codes[r][k] * scales[r][k / 128].  Grid: t is the smallest whole number >= -126 with
+ * max|x| <= 448 * 2^t over the block, the scale 2^t, the code x * 2^-t rounded to nearest even.  All steps but that rounding are
+ * exact, so the arrays depend on x alone.  Weights and activations use the same format: 1 + 1/128 bytes per value.
+ *
+ * dtype (of activations and outputs): AWQ_DTYPE_F16 or AWQ_DTYPE_BF16; moe_route takes AWQ_DTYPE_F32 as well.
+ * K (and I) are multiples of 16; the last block of a row may be shorter than 128.  Rows and N are free.  The conventions of
+ * the header hold (16-byte aligned pointers, row-major contiguous arrays, no allocation, no synchronisation), but the
+ * workspaces of these calls need no zero-fill and hold nothing from one call to the next.  A value that is NaN gives a NaN
+ * code; an infinite one is undefined behaviour.  fp8_quantize never signals its dependents early, so it may be followed by
+ * a product on the weights that it wrote, as awq_pack.
+ */
+#define AWQ_DTYPE_F16 1
+#define AWQ_DTYPE_BF16 2
+#define AWQ_DTYPE_F32 3
+#define AWQ_SCORE_SOFTMAX 1
+#define AWQ_SCORE_SIGMOID 2
+
+/* Bytes of the scales of an 8-bit matrix of R rows (the codes are R * K); SIZE_MAX for invalid sizes.  Host only. */
+size_t fp8_scale_bytes(int R, int K);
+
+/*
+ * fp8_quantize -- a 16-bit matrix (a weight, or activations) to the 8-bit format above.
+ *   d_x [R][K] of dtype, device;  d_codes [R][K], d_scales fp8_scale_bytes(R, K), device, written.
+ * Errors: AWQ_ERR_UNSUPPORTED (dtype), AWQ_ERR_INVALID_ARG (R < 1, K % 16 != 0, NULL), AWQ_ERR_MISALIGNED, AWQ_ERR_CUDA.
+ */
+awq_status fp8_quantize(const void* d_x, int dtype, int R, int K, uint8_t* d_codes, uint8_t* d_scales,
+                        awq_stream_t stream);
+
+/*
+ * w8a8_gemm -- y_mn = round(sum_k x_mk w_nk) of two 8-bit matrices on the tensor cores, which apply the scales themselves;
+ * exact products, fp32 sums (order implementation defined but the same in every call), one rounding to dtype.
+ *   x [M][K], w [N][K] 8-bit matrices, device;  d_y [M][N] of dtype, written.  1 <= M <= 2^24, N >= 1.
+ * Errors: as fp8_quantize; AWQ_ERR_UNSUPPORTED also for more tiles than 31 bits count.
+ */
+awq_status w8a8_gemm(const uint8_t* d_xcodes, const uint8_t* d_xscales, const uint8_t* d_wcodes,
+                     const uint8_t* d_wscales, void* d_y, int dtype, int M, int N, int K, awq_stream_t stream);
+
+/*
+ * w8a8_linear -- fp8_quantize of the activations into the workspace, then w8a8_gemm (the same bits as the two calls).
+ *   d_x [M][K] of dtype, device.   d_workspace: w8a8_workspace_bytes(M, N, K) bytes; calls in flight must not share it.
+ * Errors: as w8a8_gemm, and AWQ_ERR_WORKSPACE.
+ */
+awq_status w8a8_linear(const void* d_x, int dtype, const uint8_t* d_wcodes, const uint8_t* d_wscales, void* d_y, int M,
+                       int N, int K, void* d_workspace, size_t workspace_bytes, awq_stream_t stream);
+
+/* Workspace bytes of w8a8_linear (SIZE_MAX for invalid sizes). */
+size_t w8a8_workspace_bytes(int M, int N, int K);
+
+/*
+ * moe_route -- the experts of each token from the router's logits.
+ *   p = softmax(l) or 1 / (1 + e^-l);  q = p + bias (d_bias [E] fp32, NULL: 0).  With groups > 1 the experts form `groups`
+ *   runs of E / groups; a group counts the sum of its two largest q (its only q if E == groups), and only the topk_groups
+ *   groups that count most stay.  d_ids: the topk experts of largest q, largest first; d_weights: their p (not q), divided by
+ *   their sum if renorm != 0, times scale.  Equal values go by the lowest index.  A logit of -inf or NaN masks its expert: p = 0, and
+ *   it comes after every unmasked one of the groups that stay; +inf counts as the largest fp32.  With nothing left
+ *   (every chosen p is 0) the weights are 0.  The order is decided in 64 bits; weights are rounded to fp32 once.
+ *   d_logits [M][E] of dtype;  d_ids [M][topk] int32, d_weights [M][topk] fp32, written.
+ *   1 <= E <= 1024, 1 <= topk <= min(32, E), groups divides E, groups <= 32, topk <= topk_groups * E / groups.
+ * Errors: AWQ_ERR_UNSUPPORTED (dtype, score), AWQ_ERR_INVALID_ARG, AWQ_ERR_MISALIGNED, AWQ_ERR_CUDA.
+ */
+awq_status moe_route(const void* d_logits, int dtype, const float* d_bias, int M, int E, int topk, int score, int groups,
+                     int topk_groups, int renorm, float scale, int32_t* d_ids, float* d_weights, awq_stream_t stream);
+
+/*
+ * w8a8_moe -- the expert MLP of a sparse layer on the experts that moe_route (or anything else) chose:
+ *     y_m = round( sum_j w_mj  Wd[e] Q(silu(a) b) ),   a = Wg[e] Q(x_m),  b = Wu[e] Q(x_m),  e = ids_mj,
+ *   Q the 8-bit quantizer of fp8_quantize (applied to the fp32 values silu(a) b), sums in fp32, the slots j in order.
+ *   d_x [M][K] of dtype;  d_ids [M][topk] int32, d_weights [M][topk] fp32;  gate|up: 8-bit matrices [E][2 I][K], the gate
+ *   rows of an expert before its up rows;  down: [E][N][I];  d_y [M][N] of dtype, written.  An id outside 0 .. E - 1 adds nothing
+ *   (a padded token, an expert that lives elsewhere); an expert may occur twice in a row.  topk <= 32, M * topk <= 2^24.
+ *   d_workspace: w8a8_moe_workspace_bytes(...) bytes; calls in flight must not share it.
+ * Errors: as w8a8_linear.
+ */
+awq_status w8a8_moe(const void* d_x, int dtype, const int32_t* d_ids, const float* d_weights, const uint8_t* d_gu_codes,
+                    const uint8_t* d_gu_scales, const uint8_t* d_down_codes, const uint8_t* d_down_scales, void* d_y,
+                    int M, int E, int topk, int K, int I, int N, void* d_workspace, size_t workspace_bytes,
+                    awq_stream_t stream);
+
+/* Workspace bytes of w8a8_moe (SIZE_MAX for invalid sizes). */
+size_t w8a8_moe_workspace_bytes(int M, int E, int topk, int K, int I, int N);
+
 /*
  * awq_last_device_status -- synchronizes `stream`, then reads and clears the device status word that
  * kernels set when a bounded wait runs out (AWQ_ERR_DEVICE_TIMEOUT) or a factorisation met a non-positive

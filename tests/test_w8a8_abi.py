@@ -1,0 +1,89 @@
+"""Argument checks of the 8-bit operators that need no GPU: every refusal happens on the host before a launch."""
+import ctypes
+
+import pytest
+import torch
+
+import weight_only_int4_05_b200 as W
+from weight_only_int4_05_b200 import _lib, build as libbuild
+
+P, F, Z = ctypes.c_void_p, ctypes.c_void_p(0x10000), 2**64 - 1
+ODD = ctypes.c_void_p(0x10008)
+
+
+@pytest.fixture(scope="module")
+def L():
+    libbuild.build()
+    return _lib.load()
+
+
+def test_sizes(L):
+    assert L.fp8_scale_bytes(3, 16) == 12 and L.fp8_scale_bytes(3, 512) == 12 and L.fp8_scale_bytes(3, 528) == 24
+    assert L.fp8_scale_bytes(0, 512) == Z and L.fp8_scale_bytes(3, 24) == Z and L.fp8_scale_bytes(3, 0) == Z
+    assert W.fp8_scale_cols(16) == 4 and W.fp8_scale_cols(4096) == 32 and W.fp8_scale_cols(4112) == 36
+    assert L.w8a8_workspace_bytes(1, 8, 512) >= 512 + 4
+    assert L.w8a8_workspace_bytes(0, 8, 512) == Z and L.w8a8_workspace_bytes(1, 8, 520) == Z
+    assert L.w8a8_moe_workspace_bytes(4, 8, 2, 512, 256, 512) >= 8 * (512 + 256 + 4 * 512)
+    for bad in ((0, 8, 2, 512, 256, 512), (4, 0, 2, 512, 256, 512), (4, 1025, 2, 512, 256, 512),
+                (4, 8, 0, 512, 256, 512), (4, 8, 33, 512, 256, 512), (4, 8, 2, 500, 256, 512),
+                (4, 8, 2, 512, 250, 512), (4, 8, 2, 512, 256, 0), (1 << 22, 8, 8, 512, 256, 512)):
+        assert L.w8a8_moe_workspace_bytes(*bad) == Z, bad
+
+
+def test_quantize_checks(L):
+    assert L.fp8_quantize(F, 3, 4, 512, F, F, None) == 2
+    assert L.fp8_quantize(F, 0, 4, 512, F, F, None) == 2
+    assert L.fp8_quantize(F, 1, 0, 512, F, F, None) == 1
+    assert L.fp8_quantize(F, 1, 4, 504, F, F, None) == 1
+    assert L.fp8_quantize(None, 1, 4, 512, F, F, None) == 1
+    assert L.fp8_quantize(F, 1, 4, 512, F, None, None) == 1
+    assert L.fp8_quantize(ODD, 1, 4, 512, F, F, None) == 3
+    assert L.fp8_quantize(F, 2, 4, 512, F, ODD, None) == 3
+
+
+def test_linear_checks(L):
+    big = 1 << 40
+    lin = lambda x=F, dt=1, wc=F, ws=F, y=F, M=4, N=8, K=512, work=F, n=big: L.w8a8_linear(  # noqa: E731
+        x, dt, wc, ws, y, M, N, K, work, n, None)
+    assert lin(dt=3) == 2
+    assert lin(M=0) == 1 and lin(N=0) == 1 and lin(K=0) == 1 and lin(K=520) == 1 and lin(M=-1) == 1
+    assert lin(x=None) == 1 and lin(wc=None) == 1 and lin(ws=None) == 1 and lin(y=None) == 1
+    assert lin(x=ODD) == 3 and lin(wc=ODD) == 3 and lin(ws=ODD) == 3 and lin(y=ODD) == 3 and lin(work=ODD) == 3
+    assert lin(work=None) == 6 and lin(n=16) == 6
+    mm = lambda xc=F, xs=F, dt=1, M=4, N=8, K=512: L.w8a8_gemm(xc, xs, F, F, F, dt, M, N, K, None)  # noqa: E731
+    assert mm(dt=3) == 2 and mm(M=0) == 1 and mm(K=8) == 1 and mm(xs=None) == 1 and mm(xs=ODD) == 3 and mm(xc=ODD) == 3
+
+
+def test_route_checks(L):
+    route = lambda l=F, dt=3, b=None, M=4, E=64, k=4, s=1, g=1, tg=1, sc=1.0, i=F, w=F: L.moe_route(  # noqa: E731
+        l, dt, b, M, E, k, s, g, tg, 0, ctypes.c_float(sc), i, w, None)
+    assert route(dt=4) == 2 and route(s=0) == 2 and route(s=3) == 2
+    assert route(M=0) == 1 and route(E=0) == 1 and route(E=1025) == 1 and route(k=0) == 1
+    assert route(k=33) == 1 and route(E=3, k=4) == 1
+    assert route(g=0) == 1 and route(g=5, tg=1) == 1 and route(g=64, tg=64) == 1 and route(g=8, tg=9) == 1
+    assert route(g=8, tg=0) == 1 and route(g=32, tg=1) == 1          # 4 experts out of 1 group of 2
+    assert route(sc=float("nan")) == 1
+    assert route(l=None) == 1 and route(i=None) == 1 and route(w=None) == 1
+    assert route(l=ODD) == 3 and route(b=ODD) == 3 and route(i=ODD) == 3 and route(w=ODD) == 3
+
+
+def test_moe_checks(L):
+    big = 1 << 40
+    def moe(x=F, dt=1, ids=F, w=F, gc=F, gs=F, dc=F, ds=F, y=F, M=4, E=8, k=2, K=512, I=256, N=512, work=F, n=big):
+        return L.w8a8_moe(x, dt, ids, w, gc, gs, dc, ds, y, M, E, k, K, I, N, work, n, None)
+    assert moe(dt=3) == 2
+    assert moe(M=0) == 1 and moe(E=0) == 1 and moe(k=0) == 1 and moe(K=8) == 1 and moe(I=24) == 1 and moe(N=0) == 1
+    for name in ("x", "ids", "w", "gc", "gs", "dc", "ds", "y"):
+        assert moe(**{name: None}) == 1, name
+        assert moe(**{name: ODD}) == 3, name
+    assert moe(work=None) == 6 and moe(n=100) == 6 and moe(work=ODD) == 3
+
+
+def test_python_refusals_on_the_host():
+    x = torch.zeros(4, 512, dtype=torch.float16)
+    m = W.Fp8Matrix(torch.zeros(8, 512).to(torch.float8_e4m3fn), torch.zeros(8, 4, dtype=torch.uint8).view(torch.float8_e8m0fnu))
+    for call in (lambda: W.fp8_quantize(x), lambda: W.fp8_quantize(x[0]), lambda: W.w8a8_linear(x, m),
+                 lambda: W.w8a8_linear(m, m), lambda: W.moe_route(x, 4),
+                 lambda: W.w8a8_moe(x, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), m, m)):
+        with pytest.raises(ValueError):
+            call()

@@ -10,6 +10,13 @@ kernels.  The functions carry the C entry points' names.
     y  = w4a16_linear(xp, pw)                   # GEMV (decode) or tcgen05 GEMM (prefill) by M
     gu = awq_pack_gate_up(Wg, Wu, s)            # gate and up projections interleaved in one packed weight
     h  = w4a16_gate_up_silu(xp, gu)             # silu(x' Wg^T) * (x' Wu^T), one fused call
+
+8-bit weights and activations (e4m3 codes, one power-of-two scale per row and 128 columns) and expert layers:
+
+    w  = fp8_quantize(W)                        # codes and scales of a weight, or of activations
+    y  = w8a8_linear(x, w)                      # fp16 or bf16 x, quantized on the way
+    r  = moe_route(logits, topk, score="sigmoid", bias=b, groups=8, topk_groups=4, renorm=True)
+    y  = w8a8_moe(x, r.ids, r.weights, gate_up, down)
 """
 from __future__ import annotations
 
@@ -20,6 +27,8 @@ import torch
 
 from . import _lib
 from ._lib import AwqError, MODE_GEMM, MODE_GEMV, MODE_LINEAR
+from .w8a8 import (Fp8Matrix, Routing, fp8_quantize, fp8_scale_cols, moe_route, w8a8_linear, w8a8_moe,
+                   w8a8_moe_workspace_bytes, w8a8_workspace_bytes)
 
 GROUP = 128
 
@@ -29,6 +38,8 @@ __all__ = [
     "awq_last_device_status", "reserve_workspace", "lib_path", "w4a16_gemv_noalloc",
     "awq_selftest_wait_timeout", "w4a16_linear_pf", "w4a16_gemv_s", "awq_pack_gate_up", "w4a16_gate_up_silu",
     "SearchResult", "awq_search_scale", "gptq_quantize", "awq_pack3", "w3a16_gemv",
+    "Fp8Matrix", "Routing", "fp8_quantize", "fp8_scale_cols", "w8a8_linear", "w8a8_workspace_bytes", "moe_route",
+    "w8a8_moe", "w8a8_moe_workspace_bytes",
 ]
 
 

@@ -16,7 +16,8 @@ EXPORTS = (
     "awq_last_device_status", "w4a16_gemv_noalloc", "awq_selftest_wait_timeout",
     "w4a16_linear_pf", "w4a16_gemv_s", "awq_pack_gate_up", "w4a16_gate_up_silu", "awq_search_scale",
     "awq_search_workspace_bytes", "gptq_quantize", "gptq_workspace_bytes", "awq_pack_bits", "awq_packed3_sizes",
-    "awq_pack3", "w3a16_gemv",
+    "awq_pack3", "w3a16_gemv", "fp8_scale_bytes", "fp8_quantize", "w8a8_gemm", "w8a8_linear", "w8a8_workspace_bytes",
+    "moe_route", "w8a8_moe", "w8a8_moe_workspace_bytes",
 )
 
 STATUS_NAMES = {0: "AWQ_OK", 1: "AWQ_ERR_INVALID_ARG", 2: "AWQ_ERR_UNSUPPORTED", 3: "AWQ_ERR_MISALIGNED",
@@ -95,6 +96,18 @@ def load() -> ctypes.CDLL:
         lib.w4a16_workspace_bytes.argtypes = [I, I, I, I, I]
         lib.awq_last_device_status.restype = I
         lib.awq_last_device_status.argtypes = [P]
+        F = ctypes.c_float
+        for name, restype, argtypes in (
+                ("fp8_scale_bytes", Z, [I, I]),
+                ("fp8_quantize", I, [P, I, I, I, P, P, P]),
+                ("w8a8_gemm", I, [P, P, P, P, P, I, I, I, I, P]),
+                ("w8a8_linear", I, [P, I, P, P, P, I, I, I, P, Z, P]),
+                ("w8a8_workspace_bytes", Z, [I, I, I]),
+                ("moe_route", I, [P, I, P, I, I, I, I, I, I, I, F, P, P, P]),
+                ("w8a8_moe", I, [P, I, P, P, P, P, P, P, P, I, I, I, I, I, I, P, Z, P]),
+                ("w8a8_moe_workspace_bytes", Z, [I, I, I, I, I, I])):
+            getattr(lib, name).restype = restype
+            getattr(lib, name).argtypes = argtypes
         _lib = lib
         return lib
 

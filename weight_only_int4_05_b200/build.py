@@ -16,8 +16,9 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "libawq_w4a16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["api.cu", "prep.cu", "pack.cu", "gemv.cu", "gemm.cu", "noalloc.cu", "selftest.cu", "search.cu", "gptq.cu"]
-HEADERS = ["common.cuh", "internal.h"]
+SOURCES = ["api.cu", "prep.cu", "pack.cu", "gemv.cu", "gemm.cu", "noalloc.cu", "selftest.cu", "search.cu", "gptq.cu",
+           "fp8.cu", "w8a8.cu", "route.cu", "moe.cu"]
+HEADERS = ["common.cuh", "internal.h", "fp8.cuh", "w8a8.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -45,7 +46,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "--threads", "0",
            "-cudart", "static", f"-I{os.path.join(ROOT, 'include')}", "-o", tmp]
     if verbose:
         cmd.append("-Xptxas=-v")

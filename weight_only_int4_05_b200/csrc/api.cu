@@ -7,7 +7,9 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "fp8.cuh"
 #include "internal.h"
+#include "w8a8.cuh"
 
 namespace awq {
 
@@ -346,6 +348,140 @@ awq_status awq_search_scale(const uint16_t* d_W, const uint16_t* d_xcal, int N, 
   if (status == nullptr) return AWQ_ERR_CUDA;
   return search_launch(d_W, d_xcal, N, K, R, g, n_grid, d_losses, d_s, d_best, d_workspace, workspace_bytes, status,
                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---- 8-bit block-scaled operators
+static bool dtype16(int dt) { return dt == AWQ_DTYPE_F16 || dt == AWQ_DTYPE_BF16; }
+static bool size_ok(int v, int most, int multiple) { return v >= 1 && v <= most && v % multiple == 0; }
+
+size_t fp8_scale_bytes(int R, int K) {
+  if (R < 1 || !size_ok(K, kMaxK, 16)) return SIZE_MAX;
+  return (size_t)R * (size_t)fp8_scale_cols(K);
+}
+
+awq_status fp8_quantize(const void* d_x, int dtype, int R, int K, uint8_t* d_codes, uint8_t* d_scales,
+                        awq_stream_t stream) {
+  if (!dtype16(dtype)) return AWQ_ERR_UNSUPPORTED;
+  if (R < 1 || !size_ok(K, kMaxK, 16) || !d_x || !d_codes || !d_scales) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(d_x) || !aligned16(d_codes) || !aligned16(d_scales)) return AWQ_ERR_MISALIGNED;
+  return fp8_quantize_launch(d_x, dtype, R, K, d_codes, d_scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static awq_status check_w8a8(const void* x, const void* wc, const void* ws, const void* y, int dt, int M, int N, int K) {
+  if (!dtype16(dt)) return AWQ_ERR_UNSUPPORTED;
+  if (!size_ok(M, 1 << 24, 1) || !size_ok(N, kMaxN, 1) || !size_ok(K, kMaxK, 16)) return AWQ_ERR_INVALID_ARG;
+  if (!x || !wc || !ws || !y) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(wc) || !aligned16(ws) || !aligned16(y)) return AWQ_ERR_MISALIGNED;
+  return AWQ_OK;
+}
+
+static awq_status w8a8_product(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, void* y,
+                               int dt, int M, int N, int K, awq_stream_t stream) {
+  W8Args a;
+  a.xc = xc;
+  a.xs = xs;
+  a.xrows = M;
+  a.wc = wc;
+  a.wsc = ws;
+  a.N = N;
+  a.K = K;
+  a.y = y;
+  a.dt = dt;
+  a.status = device_status_ptr();
+  a.st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.status == nullptr) return AWQ_ERR_CUDA;
+  return w8a8_launch(a);
+}
+
+awq_status w8a8_gemm(const uint8_t* d_xcodes, const uint8_t* d_xscales, const uint8_t* d_wcodes,
+                     const uint8_t* d_wscales, void* d_y, int dtype, int M, int N, int K, awq_stream_t stream) {
+  awq_status st = check_w8a8(d_xcodes, d_wcodes, d_wscales, d_y, dtype, M, N, K);
+  if (st != AWQ_OK) return st;
+  if (!d_xscales) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(d_xscales)) return AWQ_ERR_MISALIGNED;
+  return w8a8_product(d_xcodes, d_xscales, d_wcodes, d_wscales, d_y, dtype, M, N, K, stream);
+}
+
+static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+size_t w8a8_workspace_bytes(int M, int N, int K) {
+  if (!size_ok(M, 1 << 24, 1) || !size_ok(N, kMaxN, 1) || !size_ok(K, kMaxK, 16)) return SIZE_MAX;
+  return up256((size_t)M * K) + up256((size_t)M * fp8_scale_cols(K));
+}
+
+awq_status w8a8_linear(const void* d_x, int dtype, const uint8_t* d_wcodes, const uint8_t* d_wscales, void* d_y, int M,
+                       int N, int K, void* d_workspace, size_t workspace_bytes, awq_stream_t stream) {
+  awq_status st = check_w8a8(d_x, d_wcodes, d_wscales, d_y, dtype, M, N, K);
+  if (st != AWQ_OK) return st;
+  if (!d_workspace || workspace_bytes < w8a8_workspace_bytes(M, N, K)) return AWQ_ERR_WORKSPACE;
+  if (!aligned16(d_workspace)) return AWQ_ERR_MISALIGNED;
+  uint8_t* xc = static_cast<uint8_t*>(d_workspace);
+  uint8_t* xs = xc + up256((size_t)M * K);
+  st = fp8_quantize_launch(d_x, dtype, M, K, xc, xs, reinterpret_cast<cudaStream_t>(stream));
+  if (st != AWQ_OK) return st;
+  return w8a8_product(xc, xs, d_wcodes, d_wscales, d_y, dtype, M, N, K, stream);
+}
+
+awq_status moe_route(const void* d_logits, int dtype, const float* d_bias, int M, int E, int topk, int score, int groups,
+                     int topk_groups, int renorm, float scale, int32_t* d_ids, float* d_weights, awq_stream_t stream) {
+  if (!dtype16(dtype) && dtype != AWQ_DTYPE_F32) return AWQ_ERR_UNSUPPORTED;
+  if (score != AWQ_SCORE_SOFTMAX && score != AWQ_SCORE_SIGMOID) return AWQ_ERR_UNSUPPORTED;
+  if (!size_ok(M, 1 << 24, 1) || !size_ok(E, 1024, 1) || topk < 1 || topk > 32 || topk > E) return AWQ_ERR_INVALID_ARG;
+  if (groups < 1 || groups > 32 || E % groups != 0 || topk_groups < 1 || topk_groups > groups ||
+      topk > topk_groups * (E / groups))
+    return AWQ_ERR_INVALID_ARG;
+  if (!(scale == scale) || !d_logits || !d_ids || !d_weights) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(d_logits) || (d_bias && !aligned16(d_bias)) || !aligned16(d_ids) || !aligned16(d_weights))
+    return AWQ_ERR_MISALIGNED;
+  return moe_route_launch(d_logits, dtype, d_bias, M, E, topk, score, groups, topk_groups, renorm, scale, d_ids,
+                          d_weights, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static bool moe_sizes_ok(int M, int E, int topk, int K, int I, int N) {
+  return size_ok(M, 1 << 24, 1) && size_ok(E, 1024, 1) && topk >= 1 && topk <= 32 && (long long)M * topk <= (1 << 24) &&
+         size_ok(K, kMaxK, 16) && size_ok(I, kMaxK, 16) && size_ok(N, kMaxN, 1) &&
+         (long long)E * 2 * I <= 0x7FFFFFFF && (long long)E * N <= 0x7FFFFFFF;
+}
+
+size_t w8a8_moe_workspace_bytes(int M, int E, int topk, int K, int I, int N) {
+  if (!moe_sizes_ok(M, E, topk, K, I, N)) return SIZE_MAX;
+  return moe_workspace_bytes(M, E, topk, K, I, N);
+}
+
+awq_status w8a8_moe(const void* d_x, int dtype, const int32_t* d_ids, const float* d_weights, const uint8_t* d_gu_codes,
+                    const uint8_t* d_gu_scales, const uint8_t* d_down_codes, const uint8_t* d_down_scales, void* d_y,
+                    int M, int E, int topk, int K, int I, int N, void* d_workspace, size_t workspace_bytes,
+                    awq_stream_t stream) {
+  if (!dtype16(dtype)) return AWQ_ERR_UNSUPPORTED;
+  if (!moe_sizes_ok(M, E, topk, K, I, N)) return AWQ_ERR_INVALID_ARG;
+  if (!d_x || !d_ids || !d_weights || !d_gu_codes || !d_gu_scales || !d_down_codes || !d_down_scales || !d_y)
+    return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(d_x) || !aligned16(d_ids) || !aligned16(d_weights) || !aligned16(d_gu_codes) ||
+      !aligned16(d_gu_scales) || !aligned16(d_down_codes) || !aligned16(d_down_scales) || !aligned16(d_y))
+    return AWQ_ERR_MISALIGNED;
+  if (!d_workspace || workspace_bytes < moe_workspace_bytes(M, E, topk, K, I, N)) return AWQ_ERR_WORKSPACE;
+  if (!aligned16(d_workspace)) return AWQ_ERR_MISALIGNED;
+  MoeArgs a;
+  a.x = static_cast<const uint16_t*>(d_x);
+  a.ids = d_ids;
+  a.weights = d_weights;
+  a.guc = d_gu_codes;
+  a.gus = d_gu_scales;
+  a.dc = d_down_codes;
+  a.ds = d_down_scales;
+  a.y = static_cast<uint16_t*>(d_y);
+  a.dt = dtype;
+  a.M = M;
+  a.E = E;
+  a.topk = topk;
+  a.K = K;
+  a.I = I;
+  a.N = N;
+  a.ws = d_workspace;
+  a.status = device_status_ptr();
+  a.st = reinterpret_cast<cudaStream_t>(stream);
+  if (a.status == nullptr) return AWQ_ERR_CUDA;
+  return moe_launch(a);
 }
 
 awq_status awq_last_device_status(awq_stream_t stream) {

@@ -1,0 +1,68 @@
+// fp8.cu -- fp8_quantize: a 16-bit matrix to e4m3 codes with one power-of-two scale per row and 128 columns.
+//
+// Bound by memory: 2 bytes read and 1 + 1/128 written per value.
+#include "fp8.cuh"
+
+namespace awq {
+
+// One warp takes 512 columns of one row: lane l holds the 8 columns at 8 l of each half (two 16-byte loads), so the
+// 16 lanes of a half warp share a block of 128 and its maximum takes four shuffles; the four scale bytes are one word.
+template <int DT>
+__global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* x, int R, int K, int SW,
+                                                           uint8_t* codes, uint32_t* scales) {
+  pdl_wait_prior_grids();
+  const int lane = threadIdx.x & 31;
+  const long long items = (long long)R * SW;
+  const long long step = (long long)gridDim.x * (blockDim.x >> 5);
+  for (long long it = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += step) {
+    const long long row = it / SW;
+    const int w = (int)(it - row * SW);
+    uint32_t word = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = w * 512 + h * 256 + lane * 8;
+      const bool in = k < K;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (in) v = ldg_stream(x + row * K + k);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      float f[8];
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = pair_to_f32<DT>(u[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+        m = fmaxf(m, fmaxf(fabsf(p.x), fabsf(p.y)));
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+      const uint32_t b = fp8_scale_byte(__float_as_uint(m));
+      const float inv = fp8_inv_scale(b);
+      if (in) {
+        uint2 c;
+        c.x = e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
+        c.y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
+        *reinterpret_cast<uint2*>(codes + row * K + k) = c;
+      }
+      const int blk = w * 4 + h * 2;
+      const uint32_t other = __shfl_sync(0xFFFFFFFFu, b, 16);  // the second block of this half, for lane 0
+      word |= (blk < fp8_blocks(K) ? b : 127u) << (16 * h);
+      word |= (blk + 1 < fp8_blocks(K) ? other : 127u) << (16 * h + 8);
+    }
+    if (lane == 0) scales[row * SW + w] = word;
+  }
+}
+
+awq_status fp8_quantize_launch(const void* x, int dt, int R, int K, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+  const int SW = fp8_scale_cols(K) / 4;
+  const long long warps = (long long)R * SW;
+  long long blocks = (warps + 7) / 8;
+  const long long cap = (long long)num_sms() * 8;
+  if (blocks > cap) blocks = cap;
+  auto kernel = dt == AWQ_DTYPE_F16 ? fp8_quantize_kernel<AWQ_DTYPE_F16> : fp8_quantize_kernel<AWQ_DTYPE_BF16>;
+  cudaError_t e = launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, st, static_cast<const uint16_t*>(x), R, K, SW,
+                             codes, reinterpret_cast<uint32_t*>(scales));
+  return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+}  // namespace awq

@@ -83,5 +83,22 @@ size_t search_workspace_bytes(int N, int K, int R, int g);
 awq_status search_launch(const uint16_t* W, const uint16_t* xcal, int N, int K, int R, int g, int n_grid,
                          double* losses, uint16_t* s_out, int* best_out, void* ws, size_t ws_bytes,
                          unsigned* status, cudaStream_t st);
+// Expert router (route.cu): arguments validated by the caller.
+awq_status moe_route_launch(const void* logits, int dt, const float* bias, int M, int E, int topk, int score, int groups,
+                            int topk_groups, int renorm, float scale, int32_t* ids, float* weights, cudaStream_t st);
+// Expert MLP (moe.cu): workspace bytes (0: too large) and the launch sequence (arguments validated by the caller).
+struct MoeArgs {
+  const uint16_t* x = nullptr;
+  const int32_t* ids = nullptr;
+  const float* weights = nullptr;
+  const uint8_t *guc = nullptr, *gus = nullptr, *dc = nullptr, *ds = nullptr;  // gate|up and down: codes, scales
+  uint16_t* y = nullptr;
+  int dt = 0, M = 0, E = 0, topk = 0, K = 0, I = 0, N = 0;
+  void* ws = nullptr;
+  unsigned* status = nullptr;
+  cudaStream_t st = nullptr;
+};
+size_t moe_workspace_bytes(int M, int E, int topk, int K, int I, int N);
+awq_status moe_launch(const MoeArgs& a);
 
 }  // namespace awq
