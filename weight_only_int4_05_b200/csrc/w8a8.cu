@@ -9,9 +9,15 @@
 // Per CTA (8 warps), persistent over output tiles, k-blocks of 128 channels through an ST-stage ring:
 //   warp 0      producer: TMA copies of the weight rows and of the tokens (128-byte swizzle) onto full[s].
 //   warp 1      MMA: per k-block 4 x tcgen05.mma (32 channels each); every 4th k-block first copies the next scale words
-//               from shared to tensor memory (tcgen05.cp, two slots).
-//   warps 2, 3  scales: one 32-bit word per row holds the scales of 4 k-blocks; each warp fills one of two slots.
+//               from shared to tensor memory (tcgen05.cp, kSf slots).
+//   warps 2, 3  scales: one 32-bit word per row holds the scales of 4 k-blocks; they fill the slots in turn.
 //   warps 4..7  epilogue: tensor memory -> registers -> y, or h = silu(gate) up quantized again.
+// Two accumulators alternate, so a tile's epilogue runs under the next tile's products; where two do not fit beside the
+// scales they share some columns, which the epilogue reads first.
+// Many tokens (CG = 2): two CTAs work on one tile of 256 weight rows; each holds its 128 rows, half of the tokens' codes and
+// its half of the accumulator, so each byte of x brought to an SM serves 256 rows.
+// Few tokens (splits > 1): a cluster shares one tile, each CTA a part of K; the partial sums meet in shared memory
+// (each CTA finishes some of the tokens, summing the parts in rank order), so there is no workspace and no counter.
 // Every mbarrier wait is bounded; a timeout is recorded in the status word, the CTA drains its copies and MMAs, frees
 // its tensor memory and exits.
 #include "fp8.cuh"
@@ -21,11 +27,14 @@ namespace awq {
 
 namespace {
 
-constexpr int kTileW = 128;        // weight rows per accumulator
+constexpr int kTileW = 128;        // weight rows per accumulator and CTA
 constexpr int kBlkBytes = 128;     // bytes of K per k-block: one swizzle row, one scale block
 constexpr int kW8Threads = 256;
 constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on sm_100
-constexpr int kMaxGroups = 1024;
+#ifndef AWQ_W8_PAIR_BT
+#define AWQ_W8_PAIR_BT 128
+#endif
+constexpr int kSf = 4;             // scale slots (4 k-blocks each) in shared and tensor memory
 
 struct W8Params {
   const uint32_t* ws;  // scale words of w and x, SW per row
@@ -37,8 +46,8 @@ struct W8Params {
   const int* tile_start;
   unsigned* status;
   int xrows, wrows, wtotal;  // rows of x, weight rows per group, weight rows in all
-  int N, K, KB, SW, SWh;
-  int BT, ST, tmem_cols, groups, n_tiles, t_tiles, dt;
+  int N, KB, SW, SWh;
+  int BT, ST, tmem_cols, acc_off, groups, n_tiles, t_tiles, splits, dt;
   uint32_t idesc;
 };
 
@@ -49,16 +58,18 @@ struct W8Tile {
 template <int EPI>
 constexpr int kAtomsA = EPI == kW8SiluQuant ? 2 : 1;  // accumulators (weight row sets) per tile
 
-__host__ __device__ constexpr int w8_stage(int atoms, int BT) { return (atoms * kTileW + BT) * kBlkBytes; }
+__host__ __device__ constexpr int w8_stage(int atoms, int x_rows) { return (atoms * kTileW + x_rows) * kBlkBytes; }
 __host__ __device__ constexpr int w8_sf_slot(int atoms, int BT) { return (atoms + (BT + 127) / 128) * 512; }
+__host__ __device__ constexpr int w8_sf_cols(int atoms, int BT) { return (atoms + (BT + 127) / 128) * 4; }
 
-// Tile number -> place.  Dense: token tiles fastest, so the tiles in flight share weight rows.  Grouped: group by group,
-// token tiles fastest within a weight tile; tabs = [tile_start | row_start] in shared memory.
-__device__ __forceinline__ W8Tile w8_tile(const W8Params& p, const int* tabs, int tile) {
+// Tile number -> place; a tile is 128 * CG weight rows.  Dense: token tiles fastest, so the tiles in flight share weight
+// rows.  Grouped: group by group, token tiles fastest within a weight tile; tabs = [tile_start | row_start].
+template <int CG>
+__device__ __forceinline__ W8Tile w8_tile(const W8Params& p, const int* tabs, int tile, int rank) {
   W8Tile r;
   if (p.groups == 0) {
     const int n = tile / p.t_tiles, t = tile - n * p.t_tiles;
-    r.n0 = n * kTileW;
+    r.n0 = n * (kTileW * CG) + (CG == 2 ? rank * kTileW : 0);
     r.w0 = r.n0;
     r.t0 = t * p.BT;
     r.rows = min(p.BT, p.xrows - r.t0);
@@ -73,7 +84,7 @@ __device__ __forceinline__ W8Tile w8_tile(const W8Params& p, const int* tabs, in
   const int local = tile - tabs[lo] * p.n_tiles;
   const int n = local / tt, t = local - n * tt;
   const int* rows = tabs + p.groups + 1;
-  r.n0 = n * kTileW;
+  r.n0 = n * (kTileW * CG) + (CG == 2 ? rank * kTileW : 0);
   r.w0 = lo * p.wrows + r.n0;
   r.t0 = rows[lo] + t * p.BT;
   r.rows = min(p.BT, rows[lo + 1] - r.t0);
@@ -86,50 +97,96 @@ struct W8Maps {
 
 __device__ __forceinline__ float w8_silu(float a) { return a / (1.0f + expf(-a)); }
 
+// Outputs of weight row n0 + row for the W tokens from column c of the tile on.
+template <int W>
+__device__ __forceinline__ void w8_store(const W8Params& p, const W8Tile& t, int row, int c, const float (&f)[W]) {
+  const int n = t.n0 + row;
+  if (n >= p.N) return;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (c + i < t.rows) {
+      const size_t at = (size_t)(t.t0 + c + i) * p.N + n;
+      if (p.dt == AWQ_DTYPE_F32) static_cast<float*>(p.y)[at] = f[i];
+      else static_cast<uint16_t*>(p.y)[at] = f32_to_16(f[i], p.dt);
+    }
+  }
+}
+
+// h = silu(a) b of the same tokens, quantized: the 128 rows of the tile are one block of the 8-bit format, so its maximum
+// is taken over the four warps' lanes.  `amax` [2][4][16] alternates by `turn`, so one barrier per call is enough.
+template <int W>
+__device__ __forceinline__ void w8_silu_quant(const W8Params& p, const W8Tile& t, int row, int c, const float (&a)[W],
+                                              const float (&b)[W], uint32_t* amax, int& turn) {
+  const int n = t.n0 + row, lane = row & 31, q = row >> 5;
+  uint32_t* buf = amax + turn * 64;
+  turn ^= 1;
+  float h[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    h[i] = n < p.N ? w8_silu(a[i]) * b[i] : 0.f;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h[i])));
+    if (lane == i) buf[q * 16 + i] = m;
+  }
+  named_barrier_sync(1, 128);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const uint32_t s = fp8_scale_byte(max(max(buf[i], buf[16 + i]), max(buf[32 + i], buf[48 + i])));
+    if (c + i < t.rows) {
+      const size_t r = (size_t)(t.t0 + c + i);
+      if (n < p.N) p.hc[r * p.N + n] = (uint8_t)e4m3x2(h[i] * fp8_inv_scale(s), 0.f);
+      if (row == 0 && n < p.N) p.hs[r * (p.SWh * 4) + t.n0 / kFp8Block] = (uint8_t)s;
+    }
+  }
+}
+
 }  // namespace
 
-template <int EPI>
+template <int EPI, int CG>
 __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_constant__ W8Maps maps, const W8Params p) {
   constexpr int NA = kAtomsA<EPI>;
   extern __shared__ uint8_t w8_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w8_smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stage = w8_stage(NA, p.BT), slot = w8_sf_slot(NA, p.BT);
-  uint8_t* sf = smem + (size_t)p.ST * stage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sf + 2 * slot);
+  const int stage = w8_stage(NA, p.BT / CG), slot = w8_sf_slot(NA, p.BT);
+  uint8_t* sf = smem + p.ST * stage;
+  float* part = reinterpret_cast<float*>(sf + kSf * slot);  // splits > 1: [NA * BT][128] partial sums
+  uint64_t* full = reinterpret_cast<uint64_t*>(part + (p.splits > 1 ? NA * p.BT * kTileW : 0));
   uint64_t* empty = full + p.ST;
   uint64_t* sf_full = empty + p.ST;
-  uint64_t* sf_empty = sf_full + 2;
-  uint64_t* acc_full = sf_empty + 2;
+  uint64_t* sf_empty = sf_full + kSf;
+  uint64_t* acc_full = sf_empty + kSf;
   uint64_t* acc_free = acc_full + 1;
   uint64_t* drain = acc_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* part_full = drain + 1;
+  uint64_t* part_free = part_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_free + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 2);  // [2] the epilogue warps' common decision
   uint32_t* amax = tmem_slot + 4;                    // [2][4][16] row maxima of the quantizing epilogue
   int* tabs = reinterpret_cast<int*>(amax + 128);    // grouped: tile_start and row_start
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = (CG == 2 || p.splits > 1) ? (int)cluster_rank() : 0;
+  const int csize = CG == 2 ? 2 : p.splits;  // CTAs that share a tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&sf_full[s], 1);
+    for (int s = 0; s < kSf; ++s) {
+      mbar_init(&sf_full[s], CG);
       mbar_init(&sf_empty[s], 1);
     }
     mbar_init(acc_full, 1);
-    mbar_init(acc_free, 4);
+    mbar_init(acc_free, 4 * CG);
     mbar_init(drain, 1);
+    mbar_init(part_full, 4 * p.splits);
+    mbar_init(part_free, 4 * p.splits);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.w);
     prefetch_tensormap(&maps.x);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, (unsigned)p.tmem_cols);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_group<CG>(tmem_slot, (unsigned)p.tmem_cols);
   if (p.groups != 0) {
     pdl_wait_prior_grids();
     for (int i = threadIdx.x; i <= p.groups; i += kW8Threads) {
@@ -139,207 +196,278 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
   }
   tc_fence_before_sync();
   __syncthreads();
+  if (csize > 1) cluster_sync();  // barriers and tensor memory of the other CTAs are ready
   tc_fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   pdl_launch_dependents();
   const int tiles = p.n_tiles * (p.groups != 0 ? tabs[p.groups] : p.t_tiles);
-  const uint32_t sf_tmem = tmem + (uint32_t)(NA * p.BT);
-  const uint32_t sf_cols = (uint32_t)(NA * 4 + (p.BT + 127) / 128 * 4);
+  const int first_tile = (int)blockIdx.x / csize, tile_step = (int)gridDim.x / csize;
+  const int srank = CG == 2 ? 0 : rank;  // this CTA's part of K
+  const int kb0 = (int)((long long)p.KB * srank / p.splits), kb1 = (int)((long long)p.KB * (srank + 1) / p.splits);
+  const uint32_t sf_tmem = tmem + (uint32_t)(p.acc_off + NA * p.BT);
+  const uint32_t sf_cols = (uint32_t)w8_sf_cols(NA, p.BT);
 
   if (warp == 0) {
     if (lane == 0) {
-      const unsigned tx = (unsigned)stage;
-      long long it = 0;
-      bool first = true;
+      int s = 0, loads = 0;   // ring position; loads saturates at ST (how many stages may be in flight)
+      unsigned phase = 1;     // parity of the empty[] phase to wait for: the first round finds its stages free
+      auto advance = [&]() {
+        if (loads < p.ST) ++loads;
+        if (++s == p.ST) {
+          s = 0;
+          phase ^= 1u;
+        }
+      };
+      const uint32_t base = smem_u32(smem);
+      // In a pair both CTAs' copies count on the even CTA's barrier, which expects the bytes of both.
+      const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : smem_u32(full);
       auto load_w = [&](const W8Tile& t, int kb, int s) {
-        uint8_t* st = smem + (size_t)s * stage;
-        mbar_arrive_expect_tx(&full[s], tx);
+        if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(CG * stage));
 #pragma unroll
         for (int a = 0; a < NA; ++a)
-          tma_load_2d(st + a * kTileW * kBlkBytes, &maps.w, kb * kBlkBytes, t.w0 + a * p.N, &full[s]);
+          tma_load_2d_group<CG>(base + s * stage + a * kTileW * kBlkBytes, &maps.w, kb * kBlkBytes, t.w0 + a * p.N,
+                                full0 + s * 8);
       };
       auto load_x = [&](const W8Tile& t, int kb, int s) {
-        tma_load_2d(smem + (size_t)s * stage + NA * kTileW * kBlkBytes, &maps.x, kb * kBlkBytes, t.t0, &full[s]);
+        tma_load_2d_group<CG>(base + s * stage + NA * kTileW * kBlkBytes, &maps.x, kb * kBlkBytes,
+                              t.t0 + (CG == 2 ? rank * (p.BT / 2) : 0), full0 + s * 8);
       };
-      for (int tile = blockIdx.x; tile < tiles && !*abort_flag; tile += gridDim.x) {
-        const W8Tile t = w8_tile(p, tabs, tile);
-        int kb = 0;
+      bool first = true, ok = true;
+      for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
+        const W8Tile t = w8_tile<CG>(p, tabs, tile, rank);
+        int kb = kb0;
         if (first) {  // weights do not depend on the kernel before this one: the first ring of them goes ahead of the wait
           first = false;
-          const int pre = min(p.ST, p.KB);
-          for (; kb < pre; ++kb) load_w(t, kb, kb);
+          const int pre = min(p.ST, kb1 - kb0);
+          for (int i = 0; i < pre; ++i) load_w(t, kb0 + i, i);
           pdl_wait_prior_grids();
-          for (kb = 0; kb < pre; ++kb) load_x(t, kb, kb);
-          it = pre;
+          for (; kb < kb0 + pre; ++kb) {
+            load_x(t, kb, s);
+            advance();
+          }
         }
-        for (; kb < p.KB; ++kb, ++it) {
-          const int s = (int)(it % p.ST);
-          if (it >= p.ST && (*abort_flag || !mbar_wait(&empty[s], (unsigned)((it / p.ST - 1) & 1), p.status))) {
+        for (; kb < kb1; ++kb) {
+          if (!mbar_try_wait(&empty[s], phase) && (*abort_flag || !mbar_wait(&empty[s], phase, p.status))) {
             *abort_flag = 1;
+            ok = false;
             break;
           }
           load_w(t, kb, s);
           load_x(t, kb, s);
+          advance();
         }
       }
-      if (*abort_flag) {  // every copy that this thread issued lands before the CTA ends
-        for (long long i = it > p.ST ? it - p.ST : 0; i < it; ++i)
-          mbar_wait(&full[i % p.ST], (unsigned)((i / p.ST) & 1), p.status);
+      if (*abort_flag) {  // copies that this thread issued land before the CTA ends
+        if (CG == 1 || rank == 0) {
+          for (; loads > 0; --loads) {
+            if (--s < 0) {
+              s = p.ST - 1;
+              phase ^= 1u;
+            }
+            mbar_wait(&full[s], phase ^ 1u, p.status);
+          }
+        } else {  // counted in the other CTA: a millisecond covers any copy
+          const unsigned long long t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+        }
       }
       pdl_wait_prior_grids();
     }
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      long long it = 0;
-      int cc = 0, done = 0;
-      for (int tile = blockIdx.x; tile < tiles && !*abort_flag; tile += gridDim.x, ++done) {
-        if (done > 0 && !mbar_wait(acc_free, (unsigned)((done - 1) & 1), p.status)) {
-          *abort_flag = 1;
-          break;
-        }
+    if (CG == 1 || rank == 0) {
+      int s = 0, cs = 0, done = 0;
+      unsigned phase = 0, cphase = 0;
+      bool ok = true;
+      const uint32_t base = smem_u32(smem), sfbase = smem_u32(sf);
+      for (int tile = first_tile; tile < tiles && ok; tile += tile_step, ++done) {
+        if (done > 0 && !warp_wait(acc_free, (unsigned)((done - 1) & 1), p.status, abort_flag)) break;
         tc_fence_after_sync();
-        for (int kb = 0; kb < p.KB; ++kb, ++it) {
-          const int s = (int)(it % p.ST), c = cc & 1;
-          const uint32_t sfa = sf_tmem + (uint32_t)c * sf_cols, sfb = sfa + NA * 4;
-          if ((kb & 3) == 0) {  // the scales of the next 4 k-blocks
-            if (*abort_flag || !mbar_wait(&sf_full[c], (unsigned)((cc >> 1) & 1), p.status)) {
-              *abort_flag = 1;
-              break;
-            }
+        const uint32_t acc = tmem + ((done & 1) ? (uint32_t)p.acc_off : 0u);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const uint32_t sfa = sf_tmem + (uint32_t)cs * sf_cols, sfb = sfa + NA * 4;
+          if ((kb & 3) == 0 || kb == kb0) {  // the scales of the next 4 k-blocks
+            if (!(ok = warp_wait(&sf_full[cs], cphase, p.status, abort_flag))) break;
             tc_fence_after_sync();
-            for (int a = 0; a * 512 < slot; ++a)
-              tmem_cp_32x128(sfa + a * 4, umma_desc_plain(smem_u32(sf + (size_t)c * slot + a * 512)));
+            if (elect_one()) {
+              const uint64_t d = umma_desc_plain(sfbase + cs * slot);
+              for (int a = 0; a * 512 < slot; ++a) tmem_cp_32x128<CG>(sfa + a * 4, d + a * 32);
+            }
+            __syncwarp();
           }
-          if (*abort_flag || !mbar_wait(&full[s], (unsigned)((it / p.ST) & 1), p.status)) {
-            *abort_flag = 1;
-            break;
-          }
+          if (!(ok = warp_wait(&full[s], phase, p.status, abort_flag))) break;
           tc_fence_after_sync();
-          const uint32_t wa = smem_u32(smem + (size_t)s * stage), xb = wa + NA * kTileW * kBlkBytes;
-          const uint32_t id = umma_idesc_sf(p.idesc, (uint32_t)(kb & 3));
+          const bool last = (kb & 3) == 3 || kb == kb1 - 1;
+          if (elect_one()) {
+            const uint64_t wa = umma_desc_sw128(base + s * stage);
+            const uint64_t xb = umma_desc_sw128(base + s * stage + NA * kTileW * kBlkBytes);
+            const uint32_t id = umma_idesc_sf(p.idesc, (uint32_t)(kb & 3));
+            // descriptors count 16 bytes: + 2 per 32 channels, + 1024 per set of 128 rows
 #pragma unroll
-          for (int a = 0; a < NA; ++a)
+            for (int a = 0; a < NA; ++a)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_mxf8(tmem + (uint32_t)(a * p.BT), umma_desc_sw128(wa + a * kTileW * kBlkBytes + k * 32),
-                        umma_desc_sw128(xb + k * 32), id, sfa + a * 4, sfb, (kb | k) != 0);
-          umma_commit(&empty[s]);
-          if ((kb & 3) == 3 || kb == p.KB - 1) {
-            umma_commit(&sf_empty[c]);
-            ++cc;
+              for (int k = 0; k < 4; ++k)
+                umma_mxf8<CG>(acc + (uint32_t)(a * p.BT), wa + a * 1024 + k * 2, xb + k * 2, id, sfa + a * 4, sfb,
+                              k > 0 || kb > kb0);
+            umma_commit_group<CG>(&empty[s]);
+            if (last) umma_commit_group<CG>(&sf_empty[cs]);
+            if (kb == kb1 - 1) umma_commit_group<CG>(acc_full);
+          }
+          __syncwarp();
+          if (++s == p.ST) {
+            s = 0;
+            phase ^= 1u;
+          }
+          if (last && ++cs == kSf) {
+            cs = 0;
+            cphase ^= 1u;
           }
         }
-        if (*abort_flag) break;
-        umma_commit(acc_full);
       }
-      umma_commit(drain);
+      if (elect_one()) umma_commit_group<CG>(drain);
+      __syncwarp();
     }
   } else if (warp < 4) {
     const int which = warp - 2;
-    int cc = 0;
+    int turn = 0, cs = 0;
+    unsigned phase = 1;
     pdl_wait_prior_grids();
     bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const W8Tile t = w8_tile(p, tabs, tile);
-      for (int c = 0; c * 4 < p.KB; ++c, ++cc) {
-        if ((cc & 1) != which) continue;
-        uint32_t va[NA][4], vb[8];
+    const int c0 = kb0 >> 2, c1 = (kb1 + 3) >> 2;
+    for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
+      const W8Tile t = w8_tile<CG>(p, tabs, tile, rank);
+      for (int c = c0; c < c1 && kb0 < kb1; ++c) {
+        if (turn == which) {
+          uint32_t va[NA][4], vb[8];
 #pragma unroll
-        for (int a = 0; a < NA; ++a)
+          for (int a = 0; a < NA; ++a)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = min(t.w0 + a * p.N + j * 32 + lane, p.wtotal - 1);
-            va[a][j] = __ldg(p.ws + (size_t)row * p.SW + c);
+            for (int j = 0; j < 4; ++j) {
+              const int row = min(t.w0 + a * p.N + j * 32 + lane, p.wtotal - 1);
+              va[a][j] = __ldg(p.ws + (size_t)row * p.SW + c);
+            }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            vb[j] = 0;
+            if (j * 32 < p.BT) vb[j] = p.xs[(size_t)min(t.t0 + j * 32 + lane, p.xrows - 1) * p.SW + c];
           }
+          if (!(ok = warp_wait(&sf_empty[cs], phase, p.status, abort_flag))) break;
+          // row i of a 512-byte atom: the words of rows i, i + 32, i + 64, i + 96
+          uint4* dst = reinterpret_cast<uint4*>(sf + cs * slot);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          vb[j] = 0;
-          if (j * 32 < p.BT) vb[j] = p.xs[(size_t)min(t.t0 + j * 32 + lane, p.xrows - 1) * p.SW + c];
+          for (int a = 0; a < NA; ++a) dst[a * 32 + lane] = make_uint4(va[a][0], va[a][1], va[a][2], va[a][3]);
+          dst[NA * 32 + lane] = make_uint4(vb[0], vb[1], vb[2], vb[3]);
+          if (p.BT > 128) dst[(NA + 1) * 32 + lane] = make_uint4(vb[4], vb[5], vb[6], vb[7]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2) mbar_arrive_cluster(cluster_addr(&sf_full[cs], 0));
+            else mbar_arrive(&sf_full[cs]);
+          }
         }
-        if (cc >= 2 && (*abort_flag || !mbar_wait_backoff(&sf_empty[which], (unsigned)(((cc >> 1) - 1) & 1), p.status)))
-          *abort_flag = 1;
-        __syncwarp();
-        if (__shfl_sync(0xFFFFFFFFu, *abort_flag, 0)) {  // one lane reads the flag for all
-          ok = false;
-          break;
+        turn ^= 1;
+        if (++cs == kSf) {
+          cs = 0;
+          phase ^= 1u;
         }
-        // row i of a 512-byte atom: the words of rows i, i + 32, i + 64, i + 96
-        uint4* dst = reinterpret_cast<uint4*>(sf + (size_t)which * slot);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) dst[a * 32 + lane] = make_uint4(va[a][0], va[a][1], va[a][2], va[a][3]);
-        dst[NA * 32 + lane] = make_uint4(vb[0], vb[1], vb[2], vb[3]);
-        if (p.BT > 128) dst[(NA + 1) * 32 + lane] = make_uint4(vb[4], vb[5], vb[6], vb[7]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_full[which]);
       }
     }
   } else {
     pdl_wait_prior_grids();
     const int q = warp & 3, row = 32 * q + lane;  // tensor-memory lanes 32 q .. 32 q + 31 are this warp's weight rows
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
-    int done = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++done) {
-      const W8Tile t = w8_tile(p, tabs, tile);
-      if (*abort_flag || !mbar_wait(acc_full, (unsigned)(done & 1), p.status)) *abort_flag = 1;
-      named_barrier_sync(1, 128);  // the four warps take the same way out: one thread reads the flag for all
-      if (threadIdx.x == 128) stop[done & 1] = *abort_flag;
+    const int chunks = p.BT / 16;
+    const int shared = (NA * p.BT - p.acc_off + 15) / 16;  // chunks whose columns the next tile's accumulator takes
+    int done = 0, turn = 0, decisions = 0;
+    // The four warps take the same way out: one thread reads the flag for all.
+    auto all_ok = [&]() {
       named_barrier_sync(1, 128);
-      if (stop[done & 1]) break;
-      tc_fence_after_sync();
-      const int n = t.n0 + row;
-      for (int c0 = 0; c0 < p.BT; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(tq + (uint32_t)c0, v);
-        if constexpr (EPI == kW8Store) {
-          tmem_wait_ld();
-          if (n < p.N) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (c0 + i < t.rows) {
-                const size_t at = (size_t)(t.t0 + c0 + i) * p.N + n;
-                const float f = __uint_as_float(v[i]);
-                if (p.dt == AWQ_DTYPE_F32) static_cast<float*>(p.y)[at] = f;
-                else static_cast<uint16_t*>(p.y)[at] = f32_to_16(f, p.dt);
-              }
-            }
-          }
-        } else {
-          uint32_t u[16];
-          tmem_ld_32x32b_x16(tq + (uint32_t)(p.BT + c0), u);
-          tmem_wait_ld();
-          const int buf = (c0 >> 4) & 1;
-          float h[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            h[i] = n < p.N ? w8_silu(__uint_as_float(v[i])) * __uint_as_float(u[i]) : 0.f;
-            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h[i])));
-            if (lane == i) amax[(buf * 4 + q) * 16 + i] = m;
-          }
-          named_barrier_sync(1, 128);  // two buffers: the next chunk's maxima do not meet this chunk's readers
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t* am = amax + buf * 64 + i;
-            const uint32_t b = fp8_scale_byte(max(max(am[0], am[16]), max(am[32], am[48])));
-            if (c0 + i < t.rows) {
-              const size_t r = (size_t)(t.t0 + c0 + i);
-              if (n < p.N) p.hc[r * p.N + n] = (uint8_t)e4m3x2(h[i] * fp8_inv_scale(b), 0.f);
-              if (row == 0) p.hs[r * (p.SWh * 4) + t.n0 / kFp8Block] = (uint8_t)b;
-            }
-          }
-        }
-      }
+      if (threadIdx.x == 128) stop[decisions & 1] = *abort_flag;
+      named_barrier_sync(1, 128);
+      return stop[decisions++ & 1] == 0;
+    };
+    auto release = [&]() {
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_free);
+      if (lane == 0) {
+        if (CG == 2) mbar_arrive_cluster(cluster_addr(acc_free, 0));
+        else mbar_arrive(acc_free);
+      }
+    };
+    for (int tile = first_tile; tile < tiles; tile += tile_step, ++done) {
+      const W8Tile t = w8_tile<CG>(p, tabs, tile, rank);
+      const bool any = kb0 < kb1;
+      if (any) warp_wait(acc_full, (unsigned)(done & 1), p.status, abort_flag);
+      if (!all_ok()) break;
+      tc_fence_after_sync();
+      const int buf = done & 1;
+      const uint32_t acc = tq + (buf ? (uint32_t)p.acc_off : 0u);
+      if (p.splits == 1) {
+        if (shared == 0) release();
+        for (int i = 0; i < chunks; ++i) {
+          const int c = 16 * (buf ? i : chunks - 1 - i);  // the shared columns are the first buffer's last, the second's first
+          uint32_t v[16], u[16];
+          tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
+          if (NA == 2) tmem_ld_32x32b_x16(acc + (uint32_t)(p.BT + c), u);
+          tmem_wait_ld();
+          if (i == shared - 1) release();
+          float f[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+          if constexpr (EPI == kW8Store) {
+            w8_store<16>(p, t, row, c, f);
+          } else {
+            float g[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) g[j] = __uint_as_float(u[j]);
+            w8_silu_quant<16>(p, t, row, c, f, g, amax, turn);
+          }
+        }
+        continue;
+      }
+      // ---- split K: the parts of all CTAs of the cluster are summed in rank order, each CTA doing its share of the tokens
+      if (done > 0) warp_wait(part_free, (unsigned)((done - 1) & 1), p.status, abort_flag);
+      for (int c = 0; c < NA * p.BT; c += 16) {
+        uint32_t v[16];
+        if (any) {
+          tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * kTileW + row] = any ? __uint_as_float(v[j]) : 0.f;
+      }
+      release();
+      if (lane == 0)
+        for (int r = 0; r < p.splits; ++r) mbar_arrive_cluster(cluster_addr(part_full, (uint32_t)r));
+      warp_wait(part_full, (unsigned)(done & 1), p.status, abort_flag);
+      if (!all_ok()) break;
+      const int share = p.BT / p.splits;  // tokens per CTA, a multiple of 2
+      for (int c = rank * share; c < (rank + 1) * share; c += 2) {
+        float f[2] = {0.f, 0.f}, g[2] = {0.f, 0.f};
+        for (int r = 0; r < p.splits; ++r) {
+          const uint32_t src = cluster_addr(part + c * kTileW + row, (uint32_t)r);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            f[j] += ld_cluster_f32(src + j * kTileW * 4);
+            if (NA == 2) g[j] += ld_cluster_f32(src + (p.BT + j) * kTileW * 4);
+          }
+        }
+        if constexpr (EPI == kW8Store) w8_store<2>(p, t, row, c, f);
+        else w8_silu_quant<2>(p, t, row, c, f, g, amax, turn);
+      }
+      __syncwarp();
+      if (lane == 0)
+        for (int r = 0; r < p.splits; ++r) mbar_arrive_cluster(cluster_addr(part_free, (uint32_t)r));
     }
   }
   tc_fence_before_sync();
   __syncthreads();
+  // In-flight products finish before tensor memory is released, and no CTA leaves while another one may still reach it.
+  if (warp == 1 && *abort_flag) mbar_wait(drain, 0, p.status);
+  if (csize > 1) cluster_sync();
   if (warp == 1) {
-    if (*abort_flag) mbar_wait(drain, 0, p.status);  // MMAs in flight finish before tensor memory is released
     tc_fence_after_sync();
-    tmem_dealloc(tmem, (unsigned)p.tmem_cols);
+    tmem_dealloc_group<CG>(tmem, (unsigned)p.tmem_cols);
   }
 }
 
@@ -373,17 +501,31 @@ bool encode_codes(EncodeTiledFn encode, CUtensorMap* map, const uint8_t* p, long
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI>
+template <int EPI, int CG>
 cudaError_t launch_one(const W8Maps& maps, const W8Params& p, int grid, int smem, cudaStream_t st) {
   static bool ready[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(w8a8_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
+    const cudaError_t e = cudaFuncSetAttribute(w8a8_kernel<EPI, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  return launch_pdl(w8a8_kernel<EPI>, dim3((unsigned)grid), dim3(kW8Threads), (size_t)smem, st, maps, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kW8Threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)(CG == 2 ? 2 : p.splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = attr[1].val.clusterDim.x > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, w8a8_kernel<EPI, CG>, maps, p);
 }
 
 }  // namespace
@@ -413,7 +555,6 @@ awq_status w8a8_launch(const W8Args& a) {
   p.xrows = a.xrows;
   p.wrows = a.N * atoms;
   p.N = a.N;
-  p.K = a.K;
   p.KB = fp8_blocks(a.K);
   p.SW = fp8_scale_cols(a.K) / 4;
   p.SWh = fp8_scale_cols(a.N) / 4;
@@ -423,30 +564,41 @@ awq_status w8a8_launch(const W8Args& a) {
   p.BT = a.groups ? a.bt : a.xrows >= most ? most : (a.xrows + 15) / 16 * 16;
   const long long wtotal = (long long)p.wrows * (a.groups ? a.groups : 1);
   p.wtotal = (int)wtotal;
-  p.n_tiles = (a.N + kTileW - 1) / kTileW;
+  const int cg = p.BT >= AWQ_W8_PAIR_BT ? 2 : 1;
+  p.n_tiles = (a.N + kTileW * cg - 1) / (kTileW * cg);
   p.t_tiles = (a.xrows + p.BT - 1) / p.BT;
   // upper bound of the tiles: grouped, each group that has rows adds at most one partly filled token tile
   const long long tt = a.groups ? (a.xrows / p.BT + (a.xrows < a.groups ? a.xrows : a.groups)) : p.t_tiles;
   const long long bound = tt * p.n_tiles;
   if (bound > 0x7FFFFFFF || wtotal > 0x7FFFFFFF) return AWQ_ERR_UNSUPPORTED;
-  const int stage = w8_stage(atoms, p.BT), slot = w8_sf_slot(atoms, p.BT);
-  const int rest = 1024 + 2 * slot + 2 * 16 * 8 + 64 + 512 + 64 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
+  const int sms = num_sms();
+  p.splits = 1;
+  if (cg == 1 && p.BT <= 32)
+    while (p.splits < 8 && bound * p.splits * 2 <= sms && p.KB >= p.splits * 4) p.splits *= 2;
+  const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
+  const int part = p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
+  const int rest = 1024 + kSf * slot + part + 512 + 64 + 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
   p.ST = (kW8Smem - rest) / stage;
   if (p.ST > 12) p.ST = 12;
-  const int cols = atoms * p.BT + 2 * (atoms * 4 + (p.BT + 127) / 128 * 4);
+  const int sfc = kSf * w8_sf_cols(atoms, p.BT), acc = atoms * p.BT;
+  p.acc_off = acc < 512 - sfc - acc ? acc : 512 - sfc - acc;
   p.tmem_cols = 32;
-  while (p.tmem_cols < cols) p.tmem_cols <<= 1;
+  while (p.tmem_cols < p.acc_off + acc + sfc) p.tmem_cols <<= 1;
   if (p.ST < 2 || p.tmem_cols > 512) return AWQ_ERR_UNSUPPORTED;
-  p.idesc = umma_idesc_mxf8(kTileW, p.BT);
+  p.idesc = umma_idesc_mxf8(kTileW * cg, p.BT);
   W8Maps maps;
   if (!encode_codes(encode, &maps.w, a.wc, wtotal, a.K, kTileW) ||
-      !encode_codes(encode, &maps.x, a.xc, a.xrows, a.K, p.BT))
+      !encode_codes(encode, &maps.x, a.xc, a.xrows, a.K, p.BT / cg))
     return AWQ_ERR_CUDA;
-  const int sms = num_sms();
-  const int grid = bound < sms ? (int)bound : sms;
+  const int csize = cg == 2 ? 2 : p.splits;
+  const long long most_units = sms / csize;
+  const int grid = (int)(bound < most_units ? bound : most_units) * csize;
   const int smem = rest + p.ST * stage;
-  const cudaError_t e = a.epi == kW8SiluQuant ? launch_one<kW8SiluQuant>(maps, p, grid, smem, a.st)
-                                              : launch_one<kW8Store>(maps, p, grid, smem, a.st);
+  const cudaError_t e = a.epi == kW8SiluQuant
+                            ? (cg == 2 ? launch_one<kW8SiluQuant, 2>(maps, p, grid, smem, a.st)
+                                       : launch_one<kW8SiluQuant, 1>(maps, p, grid, smem, a.st))
+                            : (cg == 2 ? launch_one<kW8Store, 2>(maps, p, grid, smem, a.st)
+                                       : launch_one<kW8Store, 1>(maps, p, grid, smem, a.st));
   return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
 }
 
