@@ -417,7 +417,7 @@ awq_status w8a8_linear(const void* d_x, int dtype, const uint8_t* d_wcodes, cons
   if (!aligned16(d_workspace)) return AWQ_ERR_MISALIGNED;
   uint8_t* xc = static_cast<uint8_t*>(d_workspace);
   uint8_t* xs = xc + up256((size_t)M * K);
-  st = fp8_quantize_launch(d_x, dtype, M, K, xc, xs, reinterpret_cast<cudaStream_t>(stream));
+  st = fp8_quantize_launch(d_x, dtype, M, K, xc, xs, reinterpret_cast<cudaStream_t>(stream), true);
   if (st != AWQ_OK) return st;
   return w8a8_product(xc, xs, d_wcodes, d_wscales, d_y, dtype, M, N, K, stream);
 }

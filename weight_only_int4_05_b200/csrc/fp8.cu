@@ -5,11 +5,14 @@
 
 namespace awq {
 
+// EARLY: dependents may start at once, for the caller who quantizes activations and whose next kernel waits before it reads
+// them; a weight's quantizer never signals early, so that a product behind it may prefetch weights ahead of its wait.
 // One warp takes 512 columns of one row: lane l holds the 8 columns at 8 l of each half (two 16-byte loads), so the
 // 16 lanes of a half warp share a block of 128 and its maximum takes four shuffles; the four scale bytes are one word.
-template <int DT>
+template <int DT, bool EARLY>
 __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* x, int R, int K, int SW,
                                                            uint8_t* codes, uint32_t* scales) {
+  if (EARLY) pdl_launch_dependents();
   pdl_wait_prior_grids();
   const int lane = threadIdx.x & 31;
   const long long items = (long long)R * SW;
@@ -53,13 +56,16 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* x, in
   }
 }
 
-awq_status fp8_quantize_launch(const void* x, int dt, int R, int K, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+awq_status fp8_quantize_launch(const void* x, int dt, int R, int K, uint8_t* codes, uint8_t* scales, cudaStream_t st,
+                               bool early) {
   const int SW = fp8_scale_cols(K) / 4;
   const long long warps = (long long)R * SW;
   long long blocks = (warps + 7) / 8;
   const long long cap = (long long)num_sms() * 8;
   if (blocks > cap) blocks = cap;
-  auto kernel = dt == AWQ_DTYPE_F16 ? fp8_quantize_kernel<AWQ_DTYPE_F16> : fp8_quantize_kernel<AWQ_DTYPE_BF16>;
+  auto kernel = dt == AWQ_DTYPE_F16
+                    ? (early ? fp8_quantize_kernel<AWQ_DTYPE_F16, true> : fp8_quantize_kernel<AWQ_DTYPE_F16, false>)
+                    : (early ? fp8_quantize_kernel<AWQ_DTYPE_BF16, true> : fp8_quantize_kernel<AWQ_DTYPE_BF16, false>);
   cudaError_t e = launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, st, static_cast<const uint16_t*>(x), R, K, SW,
                              codes, reinterpret_cast<uint32_t*>(scales));
   return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;

@@ -6,12 +6,12 @@
 // the same as the format's native 32 and no partial sum leaves tensor memory.  Weights are the A operand (128 rows of
 // N), tokens the B operand, so a few tokens still fill the instruction's height.
 //
-// Per CTA (8 warps), persistent over output tiles, k-blocks of 128 channels through an ST-stage ring:
+// Per CTA (12 warps), persistent over output tiles, k-blocks of 128 channels through an ST-stage ring:
 //   warp 0      producer: TMA copies of the weight rows and of the tokens (128-byte swizzle) onto full[s].
 //   warp 1      MMA: per k-block 4 x tcgen05.mma (32 channels each); every 4th k-block first copies the next scale words
-//               from shared to tensor memory (tcgen05.cp, kSf slots).
+//               from shared to tensor memory (tcgen05.cp).
 //   warps 2, 3  scales: one 32-bit word per row holds the scales of 4 k-blocks; they fill the slots in turn.
-//   warps 4..7  epilogue: tensor memory -> registers -> y, or h = silu(gate) up quantized again.
+//   warps 4..11 epilogue, two warpgroups taking 16 tokens in turn: tensor memory -> registers -> y, or h = silu(gate) up quantized again.
 // Two accumulators alternate, so a tile's epilogue runs under the next tile's products; where two do not fit beside the
 // scales they share some columns, which the epilogue reads first.
 // Many tokens (CG = 2): two CTAs work on one tile of 256 weight rows; each holds its 128 rows, half of the tokens' codes and
@@ -29,12 +29,14 @@ namespace {
 
 constexpr int kTileW = 128;        // weight rows per accumulator and CTA
 constexpr int kBlkBytes = 128;     // bytes of K per k-block: one swizzle row, one scale block
-constexpr int kW8Threads = 256;
+constexpr int kEpiGroups = 2;      // epilogue warpgroups
+constexpr int kW8Threads = 128 + 128 * kEpiGroups;
 constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on sm_100
 #ifndef AWQ_W8_PAIR_BT
 #define AWQ_W8_PAIR_BT 128
 #endif
-constexpr int kSf = 4;             // scale slots (4 k-blocks each) in shared and tensor memory
+constexpr int kSf = 4;             // scale slots (4 k-blocks each) in shared memory
+constexpr int kSfTmem = 2;         // and in tensor memory
 
 struct W8Params {
   const uint32_t* ws;  // scale words of w and x, SW per row
@@ -95,46 +97,68 @@ struct W8Maps {
   CUtensorMap w, x;
 };
 
-__device__ __forceinline__ float w8_silu(float a) { return a / (1.0f + expf(-a)); }
+// a / (1 + e^-a) to a few units of 2^-23: e^-a = 2^(hi + lo) with hi + lo = -a log2(e) carried in two parts, and the fast
+// quotient (a denominator past 2^126 gives 0; a / it is below 2^-119 there).
+__device__ __forceinline__ float w8_silu(float a) {
+  const float hi = -a * 1.44269504f;
+  const float lo = fmaf(-a, 1.44269504f, -hi) - a * 1.92596299e-8f;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi));
+  e = hi < 126.f ? fmaf(e, lo * 0.693147181f, e) : e;  // past it e may be infinite, and inf * 0 is not a number
+  return __fdividef(a, 1.0f + e);
+}
 
 // Outputs of weight row n0 + row for the W tokens from column c of the tile on.
+template <int W, typename T, typename F>
+__device__ __forceinline__ void w8_store_as(const W8Params& p, const W8Tile& t, int row, int c, const float (&f)[W], F to) {
+  T* y = static_cast<T*>(p.y) + (size_t)(t.t0 + c) * p.N + (t.n0 + row);
+  const int rows = t.rows - c;
+  if (rows >= W) {
+#pragma unroll
+    for (int i = 0; i < W; ++i, y += p.N) *y = to(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i, y += p.N)
+      if (i < rows) *y = to(f[i]);
+  }
+}
 template <int W>
 __device__ __forceinline__ void w8_store(const W8Params& p, const W8Tile& t, int row, int c, const float (&f)[W]) {
-  const int n = t.n0 + row;
-  if (n >= p.N) return;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if (c + i < t.rows) {
-      const size_t at = (size_t)(t.t0 + c + i) * p.N + n;
-      if (p.dt == AWQ_DTYPE_F32) static_cast<float*>(p.y)[at] = f[i];
-      else static_cast<uint16_t*>(p.y)[at] = f32_to_16(f[i], p.dt);
-    }
-  }
+  if (t.n0 + row >= p.N) return;
+  if (p.dt == AWQ_DTYPE_F32)
+    w8_store_as<W, float>(p, t, row, c, f, [](float v) { return v; });
+  else if (p.dt == AWQ_DTYPE_F16)
+    w8_store_as<W, __half>(p, t, row, c, f, [](float v) { return __float2half_rn(v); });
+  else
+    w8_store_as<W, __nv_bfloat16>(p, t, row, c, f, [](float v) { return __float2bfloat16_rn(v); });
 }
 
 // h = silu(a) b of the same tokens, quantized: the 128 rows of the tile are one block of the 8-bit format, so its maximum
-// is taken over the four warps' lanes.  `amax` [2][4][16] alternates by `turn`, so one barrier per call is enough.
+// is taken over the four warps of a warpgroup.  `amax` [2][4][16] alternates by `turn`, so one barrier per call is enough.
 template <int W>
 __device__ __forceinline__ void w8_silu_quant(const W8Params& p, const W8Tile& t, int row, int c, const float (&a)[W],
-                                              const float (&b)[W], uint32_t* amax, int& turn) {
+                                              const float (&b)[W], uint32_t* amax, int& turn, int bar) {
   const int n = t.n0 + row, lane = row & 31, q = row >> 5;
   uint32_t* buf = amax + turn * 64;
   turn ^= 1;
   float h[W];
+  uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     h[i] = n < p.N ? w8_silu(a[i]) * b[i] : 0.f;
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h[i])));
-    if (lane == i) buf[q * 16 + i] = m;
+    if (lane == i) mine = m;
   }
-  named_barrier_sync(1, 128);
+  if (lane < W) buf[q * 16 + lane] = mine;
+  named_barrier_sync(bar, 128);
+  uint8_t* hc = p.hc + (size_t)(t.t0 + c) * p.N + n;
+  uint8_t* hs = p.hs + (size_t)(t.t0 + c) * (p.SWh * 4) + t.n0 / kFp8Block;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const uint32_t s = fp8_scale_byte(max(max(buf[i], buf[16 + i]), max(buf[32 + i], buf[48 + i])));
-    if (c + i < t.rows) {
-      const size_t r = (size_t)(t.t0 + c + i);
-      if (n < p.N) p.hc[r * p.N + n] = (uint8_t)e4m3x2(h[i] * fp8_inv_scale(s), 0.f);
-      if (row == 0 && n < p.N) p.hs[r * (p.SWh * 4) + t.n0 / kFp8Block] = (uint8_t)s;
+    if (c + i < t.rows && n < p.N) {
+      hc[(size_t)i * p.N] = (uint8_t)e4m3x2(h[i] * fp8_inv_scale(s), 0.f);
+      if (row == 0) hs[i * (p.SWh * 4)] = (uint8_t)s;
     }
   }
 }
@@ -161,8 +185,8 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_free + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 2);  // [2] the epilogue warps' common decision
-  uint32_t* amax = tmem_slot + 4;                    // [2][4][16] row maxima of the quantizing epilogue
-  int* tabs = reinterpret_cast<int*>(amax + 128);    // grouped: tile_start and row_start
+  uint32_t* amax = tmem_slot + 4;  // [kEpiGroups][2][4][16] token maxima of the quantizing epilogue
+  int* tabs = reinterpret_cast<int*>(amax + kEpiGroups * 128);    // grouped: tile_start and row_start
 
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = (CG == 2 || p.splits > 1) ? (int)cluster_rank() : 0;
@@ -177,10 +201,10 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
       mbar_init(&sf_empty[s], 1);
     }
     mbar_init(acc_full, 1);
-    mbar_init(acc_free, 4 * CG);
+    mbar_init(acc_free, 4 * kEpiGroups * CG);
     mbar_init(drain, 1);
-    mbar_init(part_full, 4 * p.splits);
-    mbar_init(part_free, 4 * p.splits);
+    mbar_init(part_full, 4 * kEpiGroups * p.splits);
+    mbar_init(part_free, 4 * kEpiGroups * p.splits);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.w);
@@ -276,8 +300,9 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
     __syncwarp();
   } else if (warp == 1) {
     if (CG == 1 || rank == 0) {
-      int s = 0, cs = 0, done = 0;
+      int s = 0, cs = 0, ct = 0, done = 0;  // ring stage, scale slots in shared and tensor memory, tiles
       unsigned phase = 0, cphase = 0;
+      int filled = 0;                       // chunks so far, up to kSfTmem
       bool ok = true;
       const uint32_t base = smem_u32(smem), sfbase = smem_u32(sf);
       for (int tile = first_tile; tile < tiles && ok; tile += tile_step, ++done) {
@@ -285,9 +310,15 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
         tc_fence_after_sync();
         const uint32_t acc = tmem + ((done & 1) ? (uint32_t)p.acc_off : 0u);
         for (int kb = kb0; kb < kb1; ++kb) {
-          const uint32_t sfa = sf_tmem + (uint32_t)cs * sf_cols, sfb = sfa + NA * 4;
+          const uint32_t sfa = sf_tmem + (uint32_t)ct * sf_cols, sfb = sfa + NA * 4;
           if ((kb & 3) == 0 || kb == kb0) {  // the scales of the next 4 k-blocks
             if (!(ok = warp_wait(&sf_full[cs], cphase, p.status, abort_flag))) break;
+            if (filled < kSfTmem) {
+              ++filled;
+            } else {  // the products that read this tensor-memory slot last are done (kSfTmem chunks ago)
+              const int was = (cs + kSf - kSfTmem) % kSf;
+              if (!(ok = warp_wait(&sf_empty[was], was > cs ? cphase ^ 1u : cphase, p.status, abort_flag))) break;
+            }
             tc_fence_after_sync();
             if (elect_one()) {
               const uint64_t d = umma_desc_plain(sfbase + cs * slot);
@@ -318,9 +349,12 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
             s = 0;
             phase ^= 1u;
           }
-          if (last && ++cs == kSf) {
-            cs = 0;
-            cphase ^= 1u;
+          if (last) {
+            ct = ct + 1 == kSfTmem ? 0 : ct + 1;
+            if (++cs == kSf) {
+              cs = 0;
+              cphase ^= 1u;
+            }
           }
         }
       }
@@ -331,7 +365,6 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
     const int which = warp - 2;
     int turn = 0, cs = 0;
     unsigned phase = 1;
-    pdl_wait_prior_grids();
     bool ok = true;
     const int c0 = kb0 >> 2, c1 = (kb1 + 3) >> 2;
     for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
@@ -346,6 +379,7 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
               const int row = min(t.w0 + a * p.N + j * 32 + lane, p.wtotal - 1);
               va[a][j] = __ldg(p.ws + (size_t)row * p.SW + c);
             }
+          pdl_wait_prior_grids();  // x's scales come from the kernel before this one, the weight's do not
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             vb[j] = 0;
@@ -375,15 +409,17 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
   } else {
     pdl_wait_prior_grids();
     const int q = warp & 3, row = 32 * q + lane;  // tensor-memory lanes 32 q .. 32 q + 31 are this warp's weight rows
+    const int wg = (warp - 4) >> 2;
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
     const int chunks = p.BT / 16;
     const int shared = (NA * p.BT - p.acc_off + 15) / 16;  // chunks whose columns the next tile's accumulator takes
+    uint32_t* my_amax = amax + wg * 128;
     int done = 0, turn = 0, decisions = 0;
-    // The four warps take the same way out: one thread reads the flag for all.
+    // All epilogue warps take the same way out: one thread reads the flag for all.
     auto all_ok = [&]() {
-      named_barrier_sync(1, 128);
+      named_barrier_sync(1, 128 * kEpiGroups);
       if (threadIdx.x == 128) stop[decisions & 1] = *abort_flag;
-      named_barrier_sync(1, 128);
+      named_barrier_sync(1, 128 * kEpiGroups);
       return stop[decisions++ & 1] == 0;
     };
     auto release = [&]() {
@@ -396,21 +432,28 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
     };
     for (int tile = first_tile; tile < tiles; tile += tile_step, ++done) {
       const W8Tile t = w8_tile<CG>(p, tabs, tile, rank);
-      const bool any = kb0 < kb1;
-      if (any) warp_wait(acc_full, (unsigned)(done & 1), p.status, abort_flag);
+      warp_wait(acc_full, (unsigned)(done & 1), p.status, abort_flag);
       if (!all_ok()) break;
       tc_fence_after_sync();
       const int buf = done & 1;
       const uint32_t acc = tq + (buf ? (uint32_t)p.acc_off : 0u);
       if (p.splits == 1) {
-        if (shared == 0) release();
-        for (int i = 0; i < chunks; ++i) {
+        bool held = true;
+        if (wg >= shared) {
+          release();
+          held = false;
+        }
+        for (int i = wg; i < chunks; i += kEpiGroups) {
           const int c = 16 * (buf ? i : chunks - 1 - i);  // the shared columns are the first buffer's last, the second's first
           uint32_t v[16], u[16];
           tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
           if (NA == 2) tmem_ld_32x32b_x16(acc + (uint32_t)(p.BT + c), u);
           tmem_wait_ld();
-          if (i == shared - 1) release();
+          if (held && i + kEpiGroups >= shared) {
+            release();
+            held = false;
+          }
+          if (c >= t.rows) continue;  // uniform: no token of this chunk exists
           float f[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
@@ -420,21 +463,20 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
             float g[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) g[j] = __uint_as_float(u[j]);
-            w8_silu_quant<16>(p, t, row, c, f, g, amax, turn);
+            w8_silu_quant<16>(p, t, row, c, f, g, my_amax, turn, 2 + wg);
           }
         }
+        if (held) release();
         continue;
       }
       // ---- split K: the parts of all CTAs of the cluster are summed in rank order, each CTA doing its share of the tokens
       if (done > 0) warp_wait(part_free, (unsigned)((done - 1) & 1), p.status, abort_flag);
-      for (int c = 0; c < NA * p.BT; c += 16) {
+      for (int c = 16 * wg; c < NA * p.BT; c += 16 * kEpiGroups) {
         uint32_t v[16];
-        if (any) {
-          tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
-          tmem_wait_ld();
-        }
+        tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
+        tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * kTileW + row] = any ? __uint_as_float(v[j]) : 0.f;
+        for (int j = 0; j < 16; ++j) part[(c + j) * kTileW + row] = __uint_as_float(v[j]);
       }
       release();
       if (lane == 0)
@@ -442,7 +484,8 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
       warp_wait(part_full, (unsigned)(done & 1), p.status, abort_flag);
       if (!all_ok()) break;
       const int share = p.BT / p.splits;  // tokens per CTA, a multiple of 2
-      for (int c = rank * share; c < (rank + 1) * share; c += 2) {
+      for (int c = rank * share + 2 * wg; c < (rank + 1) * share; c += 2 * kEpiGroups) {
+        if (c >= t.rows) break;  // uniform
         float f[2] = {0.f, 0.f}, g[2] = {0.f, 0.f};
         for (int r = 0; r < p.splits; ++r) {
           const uint32_t src = cluster_addr(part + c * kTileW + row, (uint32_t)r);
@@ -453,7 +496,7 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
           }
         }
         if constexpr (EPI == kW8Store) w8_store<2>(p, t, row, c, f);
-        else w8_silu_quant<2>(p, t, row, c, f, g, amax, turn);
+        else w8_silu_quant<2>(p, t, row, c, f, g, my_amax, turn, 2 + wg);
       }
       __syncwarp();
       if (lane == 0)
@@ -577,10 +620,10 @@ awq_status w8a8_launch(const W8Args& a) {
     while (p.splits < 8 && bound * p.splits * 2 <= sms && p.KB >= p.splits * 4) p.splits *= 2;
   const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
   const int part = p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
-  const int rest = 1024 + kSf * slot + part + 512 + 64 + 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
+  const int rest = 1024 + kSf * slot + part + 512 + 64 + kEpiGroups * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
   p.ST = (kW8Smem - rest) / stage;
   if (p.ST > 12) p.ST = 12;
-  const int sfc = kSf * w8_sf_cols(atoms, p.BT), acc = atoms * p.BT;
+  const int sfc = kSfTmem * w8_sf_cols(atoms, p.BT), acc = atoms * p.BT;
   p.acc_off = acc < 512 - sfc - acc ? acc : 512 - sfc - acc;
   p.tmem_cols = 32;
   while (p.tmem_cols < p.acc_off + acc + sfc) p.tmem_cols <<= 1;

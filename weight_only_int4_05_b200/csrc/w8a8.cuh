@@ -31,6 +31,7 @@ struct W8Args {
 };
 int w8a8_grouped_bt(long long rows, int groups, int epi);  // token tile for `rows` rows spread over `groups` groups
 awq_status w8a8_launch(const W8Args& a);
-awq_status fp8_quantize_launch(const void* x, int dt, int R, int K, uint8_t* codes, uint8_t* scales, cudaStream_t st);
+awq_status fp8_quantize_launch(const void* x, int dt, int R, int K, uint8_t* codes, uint8_t* scales, cudaStream_t st,
+                               bool early = false);
 
 }  // namespace awq

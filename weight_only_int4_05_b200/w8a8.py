@@ -6,6 +6,7 @@ Scratch comes from torch's allocator in each call (it follows the current stream
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional, Union
 
 import torch
@@ -15,7 +16,8 @@ from ._lib import AwqError
 
 _DTYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float32: 3}
 _SCORES = {"softmax": 1, "sigmoid": 2}
-_CODES, _SCALES = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_HALF = (torch.float16, torch.bfloat16)
+_CODES, _SCALES = (torch.float8_e4m3fn,), (torch.float8_e8m0fnu,)
 
 
 class Fp8Matrix(NamedTuple):
@@ -33,42 +35,49 @@ def fp8_scale_cols(K: int) -> int:
     return (K + 511) // 512 * 4
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _library(device: torch.device):
+    """The library and the raw handle of the device's current stream; these calls take microseconds, so the handle is
+    read without building a Stream object."""
+    return _lib.load(), torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _call(fn: str, device: torch.device, *args) -> None:
+def _run(fn: str, f, device: torch.device, args) -> None:
     """Calls the library with `device` current (it launches on the current device)."""
-    f = getattr(_lib.load(), fn)
-    if device.index == torch.cuda.current_device():
-        _lib.check(f(*args), fn)
+    if device.index == torch._C._cuda_getDevice():
+        status = f(*args)
     else:
         with torch.cuda.device(device):
-            _lib.check(f(*args), fn)
+            status = f(*args)
+    if status:
+        _lib.check(status, fn)
 
 
 def _need(t: torch.Tensor, name: str, dtypes, ndim: int, device: Optional[torch.device] = None) -> None:
-    if not t.is_cuda or t.dtype not in dtypes or t.dim() != ndim or not t.is_contiguous():
+    if t.dtype not in dtypes or not t.is_cuda or t.dim() != ndim or not t.is_contiguous():
         kinds = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise ValueError(f"{name} must be a contiguous CUDA {kinds} tensor of {ndim} dimensions")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _need_matrix(m: Fp8Matrix, name: str, ndim: int, device: torch.device) -> None:
-    _need(m.codes, f"{name}.codes", (_CODES,), ndim, device)
-    _need(m.scales, f"{name}.scales", (_SCALES,), ndim, device)
-    want = (*m.codes.shape[:-1], fp8_scale_cols(m.codes.shape[-1]))
-    if tuple(m.scales.shape) != want:
-        raise ValueError(f"{name}.scales has shape {tuple(m.scales.shape)}, expected {want}")
+def _need_matrix(m: Fp8Matrix, name: str, ndim: int, device: torch.device):
+    """Checks an 8-bit matrix and returns the shape of its codes."""
+    codes, scales = m
+    _need(codes, f"{name}.codes", _CODES, ndim, device)
+    _need(scales, f"{name}.scales", _SCALES, ndim, device)
+    shape = codes.shape
+    if scales.shape[-1] != fp8_scale_cols(shape[-1]) or scales.shape[:-1] != shape[:-1]:
+        raise ValueError(f"{name}.scales has shape {tuple(scales.shape)}, expected "
+                         f"{(*shape[:-1], fp8_scale_cols(shape[-1]))}")
+    return shape
 
 
-def _output(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+def _output(out: Optional[torch.Tensor], M: int, N: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(out, "out", (dtype,), len(shape), device)
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+        return torch.empty(M, N, dtype=dtype, device=device)
+    _need(out, "out", (dtype,), 2, device)
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, N)}")
     return out
 
 
@@ -77,31 +86,32 @@ def _scratch(fn: str, need: int, workspace: Optional[torch.Tensor], device: torc
         raise AwqError(fn, 1)
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+    if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace
 
 
 def fp8_quantize(x: torch.Tensor, out: Optional[Fp8Matrix] = None) -> Fp8Matrix:
     """Codes and scales of a float16 or bfloat16 matrix [R, K], or of a stack [E, R, K] of them; K % 16 == 0."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    if len(shape) not in (2, 3):
         raise ValueError("x must have 2 or 3 dimensions")
-    _need(x, "x", (torch.float16, torch.bfloat16), x.dim())
-    K = x.shape[-1]
-    R = x.shape[0] if x.dim() == 2 else x.shape[0] * x.shape[1]
+    _need(x, "x", _HALF, len(shape))
+    K = shape[-1]
+    R = shape[0] if len(shape) == 2 else shape[0] * shape[1]
     dev = x.device
     if out is None:
-        out = Fp8Matrix(torch.empty(x.shape, dtype=_CODES, device=dev),
-                        torch.empty((*x.shape[:-1], fp8_scale_cols(K)), dtype=_SCALES, device=dev))
-    else:
-        _need_matrix(out, "out", x.dim(), dev)
-        if out.codes.shape != x.shape:
-            raise ValueError(f"out has shape {tuple(out.codes.shape)}, expected {tuple(x.shape)}")
-    _call("fp8_quantize", dev, x.data_ptr(), _DTYPES[x.dtype], R, K, out.codes.data_ptr(), out.scales.data_ptr(),
-          _stream(dev))
+        out = Fp8Matrix(torch.empty_like(x, dtype=_CODES[0]),
+                        torch.empty(*shape[:-1], fp8_scale_cols(K), dtype=_SCALES[0], device=dev))
+    elif _need_matrix(out, "out", len(shape), dev) != shape:
+        raise ValueError(f"out has shape {tuple(out.codes.shape)}, expected {tuple(shape)}")
+    lib, stream = _library(dev)
+    _run("fp8_quantize", lib.fp8_quantize, dev, (x.data_ptr(), _DTYPES[x.dtype], R, K, out.codes.data_ptr(),
+                                                 out.scales.data_ptr(), stream))
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(_lib.load().w8a8_workspace_bytes(M, N, K))
 
@@ -110,32 +120,32 @@ def w8a8_linear(x: Union[torch.Tensor, Fp8Matrix], w: Fp8Matrix, out: Optional[t
                 workspace: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """y [M, N] = x [M, K] w [N, K]^T.  x is float16 or bfloat16, quantized on the way (y has its type), or already an
     Fp8Matrix (one quantization for several weights; `dtype`, or out's, is y's type, bfloat16 unless given)."""
-    if isinstance(x, Fp8Matrix):
+    quantized = isinstance(x, Fp8Matrix)
+    if quantized:
         dev = x.codes.device
-        _need_matrix(x, "x", 2, dev)
+        M, K = _need_matrix(x, "x", 2, dev)
         dtype = dtype or (torch.bfloat16 if out is None else out.dtype)
-        if dtype not in (torch.float16, torch.bfloat16):
+        if dtype not in _HALF:
             raise ValueError(f"dtype must be float16 or bfloat16, not {dtype}")
-        M, K = x.codes.shape
     else:
-        _need(x, "x", (torch.float16, torch.bfloat16), 2)
+        _need(x, "x", _HALF, 2)
         dev = x.device
-        if dtype not in (None, x.dtype):
+        if dtype is not None and dtype != x.dtype:
             raise ValueError(f"dtype {dtype} differs from x's {x.dtype}")
         dtype = x.dtype
         M, K = x.shape
-    _need_matrix(w, "w", 2, dev)
-    N = w.codes.shape[0]
-    if w.codes.shape[1] != K:
-        raise ValueError(f"x has K={K}, w has K={w.codes.shape[1]}")
-    y = _output(out, (M, N), dtype, dev)
-    if isinstance(x, Fp8Matrix):
-        _call("w8a8_gemm", dev, x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-              y.data_ptr(), _DTYPES[dtype], M, N, K, _stream(dev))
+    N, wk = _need_matrix(w, "w", 2, dev)
+    if wk != K:
+        raise ValueError(f"x has K={K}, w has K={wk}")
+    y = _output(out, M, N, dtype, dev)
+    lib, stream = _library(dev)
+    if quantized:
+        _run("w8a8_gemm", lib.w8a8_gemm, dev, (x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(),
+                                               w.scales.data_ptr(), y.data_ptr(), _DTYPES[dtype], M, N, K, stream))
         return y
     ws = _scratch("w8a8_linear", w8a8_workspace_bytes(M, N, K), workspace, dev)
-    _call("w8a8_linear", dev, x.data_ptr(), _DTYPES[dtype], w.codes.data_ptr(), w.scales.data_ptr(), y.data_ptr(), M, N, K,
-          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev))
+    _run("w8a8_linear", lib.w8a8_linear, dev, (x.data_ptr(), _DTYPES[dtype], w.codes.data_ptr(), w.scales.data_ptr(),
+                                               y.data_ptr(), M, N, K, ws.data_ptr(), ws.nbytes, stream))
     return y
 
 
@@ -154,13 +164,16 @@ def moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", bias: Opt
             raise ValueError(f"bias has shape {tuple(bias.shape)}, expected ({E},)")
     if topk < 1 or topk > 32:
         raise AwqError("moe_route", 1)
-    ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
-    weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
-    _call("moe_route", dev, logits.data_ptr(), _DTYPES[logits.dtype], 0 if bias is None else bias.data_ptr(), M, E, topk,
-          _SCORES[score], groups, topk_groups, int(renorm), scale, ids.data_ptr(), weights.data_ptr(), _stream(dev))
+    ids = torch.empty(M, topk, dtype=torch.int32, device=dev)
+    weights = torch.empty(M, topk, dtype=torch.float32, device=dev)
+    lib, stream = _library(dev)
+    _run("moe_route", lib.moe_route, dev, (
+        logits.data_ptr(), _DTYPES[logits.dtype], None if bias is None else bias.data_ptr(), M, E, topk, _SCORES[score],
+        groups, topk_groups, bool(renorm), scale, ids.data_ptr(), weights.data_ptr(), stream))
     return Routing(ids, weights)
 
 
+@functools.lru_cache(maxsize=4096)
 def w8a8_moe_workspace_bytes(M: int, E: int, topk: int, K: int, I: int, N: int) -> int:
     return int(_lib.load().w8a8_moe_workspace_bytes(M, E, topk, K, I, N))
 
@@ -169,23 +182,23 @@ def w8a8_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up:
              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [M, N] = sum over a token's slots of weights * down[e] Q(silu(gate[e] x) * up[e] x), e = ids.  gate_up
     [E, 2 I, K] (gate rows first), down [E, N, I]; an id outside 0 .. E - 1 adds nothing."""
-    _need(x, "x", (torch.float16, torch.bfloat16), 2)
+    _need(x, "x", _HALF, 2)
     dev = x.device
     M, K = x.shape
     _need(ids, "ids", (torch.int32,), 2, dev)
     _need(weights, "weights", (torch.float32,), 2, dev)
-    _need_matrix(gate_up, "gate_up", 3, dev)
-    _need_matrix(down, "down", 3, dev)
-    E, two_i, gk = gate_up.codes.shape
+    E, two_i, gk = _need_matrix(gate_up, "gate_up", 3, dev)
+    de, N, I = _need_matrix(down, "down", 3, dev)
     topk = ids.shape[1]
     if ids.shape[0] != M or weights.shape != ids.shape:
         raise ValueError(f"ids {tuple(ids.shape)} and weights {tuple(weights.shape)} do not match {M} tokens")
-    if gk != K or two_i % 2 != 0 or down.codes.shape[0] != E or down.codes.shape[2] * 2 != two_i:
+    if gk != K or de != E or 2 * I != two_i:
         raise ValueError(f"gate_up {tuple(gate_up.codes.shape)} and down {tuple(down.codes.shape)} do not match x's K={K}")
-    N, I = down.codes.shape[1:]
-    y = _output(out, (M, N), x.dtype, dev)
+    y = _output(out, M, N, x.dtype, dev)
     ws = _scratch("w8a8_moe", w8a8_moe_workspace_bytes(M, E, topk, K, I, N), workspace, dev)
-    _call("w8a8_moe", dev, x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(), weights.data_ptr(), gate_up.codes.data_ptr(),
-          gate_up.scales.data_ptr(), down.codes.data_ptr(), down.scales.data_ptr(), y.data_ptr(), M, E, topk, K, I, N,
-          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev))
+    lib, stream = _library(dev)
+    _run("w8a8_moe", lib.w8a8_moe, dev, (
+        x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(), weights.data_ptr(), gate_up.codes.data_ptr(),
+        gate_up.scales.data_ptr(), down.codes.data_ptr(), down.scales.data_ptr(), y.data_ptr(), M, E, topk, K, I, N,
+        ws.data_ptr(), ws.nbytes, stream))
     return y
