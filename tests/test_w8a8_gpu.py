@@ -363,3 +363,34 @@ def test_weight_quantized_just_before_its_use():
         got.append(W.w8a8_linear(x, buf))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[i % 2]) for i, y in enumerate(got))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("use_bias", [False, True])
+@pytest.mark.parametrize("spread", [2.0 ** -20, 1e-3, 30.0])
+def test_route_close_scores(score, use_bias, spread):
+    """Logits so close that 32-bit scores cannot order them, with few values (many true ties), and far apart."""
+    rng = np.random.default_rng(41)
+    M, E = 120, 96
+    l = torch.from_numpy(1.0 + spread * rng.integers(-8, 9, (M, E)) * (1 + (rng.random((M, E)) < 0.3))).float()
+    bias = torch.from_numpy(rng.integers(-2, 3, E) * 2.0 ** -22).float() if use_bias else None
+    for groups, tg, topk in ((1, 1, 7), (8, 3, 7), (3, 2, 32)):
+        kw = dict(topk=topk, score=score, groups=groups, topk_groups=tg, renorm=True)
+        r = W.moe_route(l.cuda(), bias=None if bias is None else bias.cuda(), **kw)
+        check_route(r, np64(l), bias=None if bias is None else np64(bias), **kw)
+
+
+def test_route_tie_at_the_border_hides_a_better_expert():
+    """Equal 32-bit scores of two kinds of experts, the kind that is better in 64 bits behind the border: by its index it would
+    be left out."""
+    E = 64
+    l = np.full((4, E), 1.0, np.float32)
+    bias = np.zeros(E, np.float32)
+    bias[40:50] = 2.0 ** -27  # half a step of a score of 0.73: lost in 32 bits
+    r = W.moe_route(torch.from_numpy(l).cuda(), 6, score="sigmoid", bias=torch.from_numpy(bias).cuda())
+    assert r.ids.cpu().tolist() == [[40, 41, 42, 43, 44, 45]] * 4
+    bias[:] = 0
+    bias[3] = -np.inf
+    bias[7] = np.nan
+    r = W.moe_route(torch.from_numpy(l).cuda(), 32, score="softmax", bias=torch.from_numpy(bias).cuda())
+    assert r.ids.cpu().tolist() == [[e for e in range(E) if e not in (3, 7)][:32]] * 4
