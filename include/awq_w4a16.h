@@ -419,8 +419,10 @@ awq_status w8a8_gemm(const uint8_t* d_xcodes, const uint8_t* d_xscales, const ui
                      const uint8_t* d_wscales, void* d_y, int dtype, int M, int N, int K, awq_stream_t stream);
 
 /*
- * w8a8_linear -- fp8_quantize of the activations into the workspace, then w8a8_gemm (the same bits as the two calls).
- *   d_x [M][K] of dtype, device.   d_workspace: w8a8_workspace_bytes(M, N, K) bytes; calls in flight must not share it.
+ * w8a8_linear -- fp8_quantize of the activations, then w8a8_gemm (the same bits as the two calls).  Up to 16 tokens the
+ * product quantizes x on its way; more are quantized into the workspace first.
+ *   d_x [M][K] of dtype, device.   d_workspace: w8a8_workspace_bytes(M, N, K) bytes (0 up to 16 tokens: it may be NULL
+ *   then); calls in flight must not share it.
  * Errors: as w8a8_gemm, and AWQ_ERR_WORKSPACE.
  */
 awq_status w8a8_linear(const void* d_x, int dtype, const uint8_t* d_wcodes, const uint8_t* d_wscales, void* d_y, int M,

@@ -21,7 +21,8 @@ def test_sizes(L):
     assert L.fp8_scale_bytes(3, 16) == 12 and L.fp8_scale_bytes(3, 512) == 12 and L.fp8_scale_bytes(3, 528) == 24
     assert L.fp8_scale_bytes(0, 512) == Z and L.fp8_scale_bytes(3, 24) == Z and L.fp8_scale_bytes(3, 0) == Z
     assert W.fp8_scale_cols(16) == 4 and W.fp8_scale_cols(4096) == 32 and W.fp8_scale_cols(4112) == 36
-    assert L.w8a8_workspace_bytes(1, 8, 512) >= 512 + 4
+    assert L.w8a8_workspace_bytes(17, 8, 512) >= 17 * (512 + 4)
+    assert L.w8a8_workspace_bytes(16, 8, 512) == 0  # the product quantizes few tokens itself
     assert L.w8a8_workspace_bytes(0, 8, 512) == Z and L.w8a8_workspace_bytes(1, 8, 520) == Z
     assert L.w8a8_moe_workspace_bytes(4, 8, 2, 512, 256, 512) >= 8 * (512 + 256 + 4 * 512)
     for bad in ((0, 8, 2, 512, 256, 512), (4, 0, 2, 512, 256, 512), (4, 1025, 2, 512, 256, 512),
@@ -43,7 +44,7 @@ def test_quantize_checks(L):
 
 def test_linear_checks(L):
     big = 1 << 40
-    lin = lambda x=F, dt=1, wc=F, ws=F, y=F, M=4, N=8, K=512, work=F, n=big: L.w8a8_linear(  # noqa: E731
+    lin = lambda x=F, dt=1, wc=F, ws=F, y=F, M=40, N=8, K=512, work=F, n=big: L.w8a8_linear(  # noqa: E731
         x, dt, wc, ws, y, M, N, K, work, n, None)
     assert lin(dt=3) == 2
     assert lin(M=0) == 1 and lin(N=0) == 1 and lin(K=0) == 1 and lin(K=520) == 1 and lin(M=-1) == 1

@@ -394,3 +394,23 @@ def test_route_tie_at_the_border_hides_a_better_expert():
     bias[7] = np.nan
     r = W.moe_route(torch.from_numpy(l).cuda(), 32, score="softmax", bias=torch.from_numpy(bias).cuda())
     assert r.ids.cpu().tolist() == [[e for e in range(E) if e not in (3, 7)][:32]] * 4
+
+
+@pytest.mark.parametrize("E", [700, 760, 1024])
+@pytest.mark.parametrize("M", [20, 700])
+def test_moe_many_experts(E, M):
+    """Expert counts whose tables come near the default shared memory, one chunk of copies and more than one."""
+    rng = np.random.default_rng(E + M)
+    check_moe(M, E, 2, 32, 16, 24, torch.bfloat16, torch.from_numpy(rng.integers(0, E, (M, 2))).int(), rng)
+
+
+@pytest.mark.parametrize("M", [3, 15, 16, 17, 32, 33, 48])
+@pytest.mark.parametrize("K", [400, 1536])
+def test_linear_either_side_of_the_fused_quantizer(M, K):
+    """Up to 16 tokens the product quantizes x itself: the same bits as from the quantizer's arrays."""
+    rng = np.random.default_rng(M + K)
+    w, wv = matrix(rng, (520, K))
+    x = activations(rng, M, K, torch.float16)
+    y = W.w8a8_linear(x.cuda(), w)
+    check_linear(y, R.grid(np64(x)), wv, torch.float16)
+    assert torch.equal(y, W.w8a8_linear(W.fp8_quantize(x.cuda()), w, dtype=torch.float16))

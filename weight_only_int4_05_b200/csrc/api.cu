@@ -376,8 +376,10 @@ static awq_status check_w8a8(const void* x, const void* wc, const void* ws, cons
 }
 
 static awq_status w8a8_product(const uint8_t* xc, const uint8_t* xs, const uint8_t* wc, const uint8_t* ws, void* y,
-                               int dt, int M, int N, int K, awq_stream_t stream) {
+                               int dt, int M, int N, int K, awq_stream_t stream, const uint16_t* x = nullptr) {
   W8Args a;
+  a.x = x;
+  a.xdt = dt;
   a.xc = xc;
   a.xs = xs;
   a.xrows = M;
@@ -406,6 +408,7 @@ static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 size_t w8a8_workspace_bytes(int M, int N, int K) {
   if (!size_ok(M, 1 << 24, 1) || !size_ok(N, kMaxN, 1) || !size_ok(K, kMaxK, 16)) return SIZE_MAX;
+  if (w8a8_quantizes(M)) return 0;  // the product quantizes few tokens itself
   return up256((size_t)M * K) + up256((size_t)M * fp8_scale_cols(K));
 }
 
@@ -413,6 +416,9 @@ awq_status w8a8_linear(const void* d_x, int dtype, const uint8_t* d_wcodes, cons
                        int N, int K, void* d_workspace, size_t workspace_bytes, awq_stream_t stream) {
   awq_status st = check_w8a8(d_x, d_wcodes, d_wscales, d_y, dtype, M, N, K);
   if (st != AWQ_OK) return st;
+  if (w8a8_quantizes(M))
+    return w8a8_product(nullptr, nullptr, d_wcodes, d_wscales, d_y, dtype, M, N, K, stream,
+                        static_cast<const uint16_t*>(d_x));
   if (!d_workspace || workspace_bytes < w8a8_workspace_bytes(M, N, K)) return AWQ_ERR_WORKSPACE;
   if (!aligned16(d_workspace)) return AWQ_ERR_MISALIGNED;
   uint8_t* xc = static_cast<uint8_t*>(d_workspace);

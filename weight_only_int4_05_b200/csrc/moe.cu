@@ -4,8 +4,9 @@
 // with Q the 8-bit quantizer (fp8.cuh).  A token's copies are sorted by expert (stable, so the order does not depend on
 // timing), quantized straight into that order, and met with the experts' weights by the grouped product of w8a8.cu; its
 // first pass ends in silu(gate) up quantized again, its second in 32-bit rows that the combine sums slot by slot.
-// Kernels: rank_kernel (rank of each copy within its expert, by chunks of 1024), place_kernel (the tables of the grouped
-// product; one launch with rank_kernel when there is one chunk), scatter_kernel, 2 x w8a8_kernel, combine_kernel.
+// Kernels: up to 1024 copies plan_kernel (ranks, tables and the quantized rows in one launch); more, rank_kernel (rank of
+// each copy within its expert, by chunks of 1024), place_kernel (the tables of the grouped product) and scatter_kernel (quantizes
+// into the sorted order); then 2 x w8a8_kernel and combine_kernel.
 #include "fp8.cuh"
 #include "w8a8.cuh"
 
@@ -52,18 +53,13 @@ Layout layout(int M, int E, int topk, int K, int I, int N) {
   return l;
 }
 
-// Exclusive sums over the chunks of each expert, over the experts, and of their token tiles.  1024 threads, E <= 1024.
-__device__ __forceinline__ void place_tables(const Plan& t, int E, int chunks, int bt_gu, int bt_d) {
+// Exclusive sums of the experts' counts (count [E] in shared memory, replaced by each expert's first row) and of their
+// token tiles, written to the tables where `write`.  1024 threads, E <= 1024.
+__device__ __forceinline__ void place_tables(const Plan& t, int E, int bt_gu, int bt_d, int* count, bool write) {
   __shared__ int warp_sum[3][32];
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
-  int count = 0;
-  if (e < E)
-    for (int c = 0; c < chunks; ++c) {
-      const int v = t.hist[(size_t)c * E + e];
-      t.hist[(size_t)c * E + e] = count;
-      count += v;
-    }
-  int v[3] = {count, (count + bt_gu - 1) / bt_gu, (count + bt_d - 1) / bt_d};
+  const int n = e < E ? count[e] : 0;
+  int v[3] = {n, (n + bt_gu - 1) / bt_gu, (n + bt_d - 1) / bt_d};
   int* out[3] = {t.row_start, t.tiles_gu, t.tiles_d};
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -81,56 +77,158 @@ __device__ __forceinline__ void place_tables(const Plan& t, int E, int chunks, i
   for (int i = 0; i < 3; ++i) {
     int before = 0;
     for (int w = 0; w < warp; ++w) before += warp_sum[i][w];
-    if (e < E) out[i][e + 1] = before + v[i];
-    if (e == 0) out[i][0] = 0;
+    if (write && e < E) out[i][e + 1] = before + v[i];
+    if (write && e == 0) out[i][0] = 0;
+    if (i == 0 && e < E) count[e] = before + v[i] - n;
   }
+  __syncthreads();
 }
 
-}  // namespace
-
-// Stable rank of each copy among the copies of its expert in this chunk of 1024: lanes of one warp by match, warps by a
-// scan of their counts.  The counts of the chunk go to hist; a single chunk writes the tables here as well.
-__global__ void __launch_bounds__(kChunk) rank_kernel(const int32_t* ids, int A, int E, Plan t, int single,
-                                                      int bt_gu, int bt_d) {
-  extern __shared__ uint16_t wcnt[];  // [32][E]
-  pdl_launch_dependents();
-  pdl_wait_prior_grids();
+// Stable rank of this thread's copy (expert e, -1: none) among the copies of its expert in the chunk: lanes of one warp by
+// match, warps by a scan of their counts in wcnt [32][E]; total [E] gets the chunk's counts.
+__device__ __forceinline__ int rank_chunk(int e, int E, uint16_t* wcnt, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < 32 * E; i += kChunk) wcnt[i] = 0;
   __syncthreads();
-  const long long a = (long long)blockIdx.x * kChunk + threadIdx.x;
-  int e = a < A ? ids[a] : -1;
-  if (e < 0 || e >= E) e = -1;
   const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e);
   const int below = __popc(peers & ((1u << lane) - 1u));
   if (e >= 0 && below == 0) wcnt[warp * E + e] = (uint16_t)__popc(peers);
   __syncthreads();
   for (int i = threadIdx.x; i < E; i += kChunk) {
     int sum = 0;
+#pragma unroll 8
     for (int w = 0; w < 32; ++w) {
       const int v = wcnt[w * E + i];
       wcnt[w * E + i] = (uint16_t)sum;
       sum += v;
     }
-    t.hist[(size_t)blockIdx.x * E + i] = sum;
+    total[i] = sum;
   }
   __syncthreads();
-  if (a < A) t.rank[a] = e < 0 ? -1 : wcnt[warp * E + e] + below;
-  if (single) place_tables(t, E, 1, bt_gu, bt_d);
+  return e < 0 ? -1 : wcnt[warp * E + e] + below;
 }
 
-__global__ void __launch_bounds__(1024) place_kernel(Plan t, int E, int chunks, int bt_gu, int bt_d) {
+// 512 columns of one token (from column 512 w on) quantized by a warp: two pieces of 8 codes per lane, and lane 0's word of
+// scales (the layout of fp8_quantize_kernel).
+template <int DT>
+__device__ __forceinline__ uint32_t quantize_512(const uint16_t* x, int K, int w, int lane, uint2 (&c)[2]) {
+  uint4 v[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int k = w * 512 + h * 256 + lane * 8;
+    v[h] = make_uint4(0u, 0u, 0u, 0u);
+    if (k < K) v[h] = ldg_stream(x + k);
+  }
+  uint32_t word = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t u[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+    float f[8], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = pair_to_f32<DT>(u[i]);
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+      m = fmaxf(m, fmaxf(fabsf(p.x), fabsf(p.y)));
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const uint32_t b = fp8_scale_byte(__float_as_uint(m));
+    const float inv = fp8_inv_scale(b);
+    c[h].x = e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
+    c[h].y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
+    word |= (b | (__shfl_sync(0xFFFFFFFFu, b, 16) << 8)) << (16 * h);  // lane 0's word: the blocks of lanes 0 and 16
+  }
+  return word;
+}
+
+// Writes a token's 512 columns to the sorted rows of its copies; lane j holds copy j's row (-1: none).
+__device__ __forceinline__ void write_copies(int to, int topk, int K, int SW, int w, int lane, const uint2 (&c)[2],
+                                             uint32_t word, uint8_t* codes, uint32_t* scales) {
+  for (int j = 0; j < topk; ++j) {
+    const int r = __shfl_sync(0xFFFFFFFFu, to, j);
+    if (r < 0) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = w * 512 + h * 256 + lane * 8;
+      if (k < K) *reinterpret_cast<uint2*>(codes + (size_t)r * K + k) = c[h];
+    }
+    if (lane == 0) scales[(size_t)r * SW + w] = word;
+  }
+}
+
+}  // namespace
+
+// Up to 1024 copies: every block ranks all of them (a few microseconds, less than a launch between two kernels) and then
+// quantizes its share of the tokens; block 0 writes the tables.
+template <int DT>
+__global__ void __launch_bounds__(kChunk) plan_kernel(const uint16_t* x, const int32_t* ids, int A, int E, int M, int topk,
+                                                      int K, int SW, Plan t, int bt_gu, int bt_d, uint8_t* codes,
+                                                      uint32_t* scales) {
+  extern __shared__ uint16_t wcnt[];  // [32][E]
+  __shared__ int first_row[kChunk], row_of[kChunk];
   pdl_launch_dependents();
   pdl_wait_prior_grids();
-  place_tables(t, E, chunks, bt_gu, bt_d);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, a = threadIdx.x;
+  int e = a < A ? ids[a] : -1;
+  if (e < 0 || e >= E) e = -1;
+  const int rank = rank_chunk(e, E, wcnt, first_row);
+  place_tables(t, E, bt_gu, bt_d, first_row, blockIdx.x == 0);
+  row_of[a] = e < 0 ? -1 : first_row[e] + rank;
+  if (blockIdx.x == 0 && a < A) t.pos[a] = row_of[a];
+  __syncthreads();
+  const int items = M * SW;
+  for (int it = blockIdx.x * 32 + warp; it < items; it += gridDim.x * 32) {
+    const int row = it / SW, w = it - row * SW;
+    uint2 c[2];
+    const uint32_t word = quantize_512<DT>(x + (size_t)row * K, K, w, lane, c);
+    write_copies(lane < topk ? row_of[row * topk + lane] : -1, topk, K, SW, w, lane, c, word, codes, scales);
+  }
 }
 
-// Quantizes each token once and writes it to the sorted rows of all its copies (the layout of fp8_quantize_kernel: one
-// warp per 512 columns of a token).
+__global__ void __launch_bounds__(kChunk) rank_kernel(const int32_t* ids, int A, int E, Plan t) {
+  extern __shared__ uint16_t wcnt[];  // [32][E]
+  __shared__ int total[kChunk];
+  pdl_launch_dependents();
+  pdl_wait_prior_grids();
+  const int a = blockIdx.x * kChunk + threadIdx.x;
+  int e = a < A ? ids[a] : -1;
+  if (e < 0 || e >= E) e = -1;
+  const int rank = rank_chunk(e, E, wcnt, total);
+  if (a < A) t.rank[a] = rank;
+  for (int i = threadIdx.x; i < E; i += kChunk) t.hist[(size_t)blockIdx.x * E + i] = total[i];
+}
+
+// Exclusive sums over the chunks of each expert (a warp per expert, a lane per chunk), then the tables.
+__global__ void __launch_bounds__(1024) place_kernel(Plan t, int E, int chunks, int bt_gu, int bt_d) {
+  __shared__ int count[1024];
+  pdl_launch_dependents();
+  pdl_wait_prior_grids();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int x = warp; x < E; x += 32) {
+    int total = 0;
+    for (int c0 = 0; c0 < chunks; c0 += 32) {
+      const int c = c0 + lane;
+      const int v = c < chunks ? t.hist[(size_t)c * E + x] : 0;
+      int s = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+        if (lane >= d) s += o;
+      }
+      if (c < chunks) t.hist[(size_t)c * E + x] = total + s - v;
+      total += __shfl_sync(0xFFFFFFFFu, s, 31);
+    }
+    if (lane == 0) count[x] = total;
+  }
+  __syncthreads();
+  place_tables(t, E, bt_gu, bt_d, count, true);
+}
+
+// Quantizes each token once and writes it to the sorted rows of all its copies, one warp per 512 columns of a token.
 template <int DT>
-__global__ void __launch_bounds__(256) scatter_kernel(const uint16_t* x, const int32_t* ids,
-                                                      int M, int E, int topk, int K, int SW, Plan t,
-                                                      uint8_t* codes, uint32_t* scales) {
+__global__ void __launch_bounds__(256) scatter_kernel(const uint16_t* x, const int32_t* ids, int M, int E, int topk, int K,
+                                                      int SW, Plan t, uint8_t* codes, uint32_t* scales) {
   pdl_launch_dependents();
   pdl_wait_prior_grids();
   const int lane = threadIdx.x & 31;
@@ -149,41 +247,9 @@ __global__ void __launch_bounds__(256) scatter_kernel(const uint16_t* x, const i
       }
       if (w == 0) t.pos[a] = to;
     }
-    uint32_t word = 0;
     uint2 c[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = w * 512 + h * 256 + lane * 8;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (k < K) v = ldg_stream(x + row * K + k);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      float f[8];
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 p = pair_to_f32<DT>(u[i]);
-        f[2 * i] = p.x;
-        f[2 * i + 1] = p.y;
-        m = fmaxf(m, fmaxf(fabsf(p.x), fabsf(p.y)));
-      }
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-      const uint32_t b = fp8_scale_byte(__float_as_uint(m));
-      const float inv = fp8_inv_scale(b);
-      c[h].x = e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
-      c[h].y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
-      word |= (b | (__shfl_sync(0xFFFFFFFFu, b, 16) << 8)) << (16 * h);  // lane 0's word: the blocks of lanes 0 and 16
-    }
-    for (int j = 0; j < topk; ++j) {
-      const int r = __shfl_sync(0xFFFFFFFFu, to, j);
-      if (r < 0) continue;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = w * 512 + h * 256 + lane * 8;
-        if (k < K) *reinterpret_cast<uint2*>(codes + (size_t)r * K + k) = c[h];
-      }
-      if (lane == 0) scales[(size_t)r * SW + w] = word;
-    }
+    const uint32_t word = quantize_512<DT>(x + row * K, K, w, lane, c);
+    write_copies(to, topk, K, SW, w, lane, c, word, codes, scales);
   }
 }
 
@@ -238,20 +304,30 @@ awq_status moe_launch(const MoeArgs& a) {
                reinterpret_cast<int*>(ws + l.tiles_gu), reinterpret_cast<int*>(ws + l.tiles_d)};
   const int bt_gu = w8a8_grouped_bt(A, a.E, kW8SiluQuant), bt_d = w8a8_grouped_bt(A, a.E, kW8Store);
   const size_t cnt = (size_t)32 * a.E * sizeof(uint16_t);  // at most 64 KB
-  if (cnt > 48 * 1024 &&
-      cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess)
+  auto plan = a.dt == AWQ_DTYPE_F16 ? plan_kernel<AWQ_DTYPE_F16> : plan_kernel<AWQ_DTYPE_BF16>;
+  if (cnt > 32 * 1024 &&  // with the static tables the default limit is near
+      (cudaFuncSetAttribute(rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess ||
+       cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess))
     return AWQ_ERR_CUDA;
-  cudaError_t e = launch_pdl(rank_kernel, dim3((unsigned)chunks), dim3(kChunk), cnt, a.st, a.ids, A, a.E, t,
-                             chunks == 1 ? 1 : 0, bt_gu, bt_d);
-  if (e == cudaSuccess && chunks > 1)
-    e = launch_pdl(place_kernel, dim3(1), dim3(1024), 0, a.st, t, a.E, chunks, bt_gu, bt_d);
-  if (e != cudaSuccess) return AWQ_ERR_CUDA;
-  const int SW = fp8_scale_cols(a.K) / 4;
-  const long long cap = (long long)num_sms() * 8;
-  long long blocks = ((long long)a.M * SW + 7) / 8;
-  auto scatter = a.dt == AWQ_DTYPE_F16 ? scatter_kernel<AWQ_DTYPE_F16> : scatter_kernel<AWQ_DTYPE_BF16>;
-  e = launch_pdl(scatter, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, a.st, a.x, a.ids, a.M, a.E, a.topk,
-                 a.K, SW, t, ws + l.xc, reinterpret_cast<uint32_t*>(ws + l.xs));
+  const int SW = fp8_scale_cols(a.K) / 4, sms = num_sms();
+  const long long cap = (long long)sms * 8;
+  const long long warps = (long long)a.M * SW;
+  long long blocks = (warps + 31) / 32;
+  uint32_t* xs = reinterpret_cast<uint32_t*>(ws + l.xs);
+  cudaError_t e;
+  if (chunks == 1) {
+    e = launch_pdl(plan, dim3((unsigned)(blocks < sms ? blocks : sms)), dim3(kChunk), cnt, a.st, a.x, a.ids, A, a.E, a.M,
+                   a.topk, a.K, SW, t, bt_gu, bt_d, ws + l.xc, xs);
+  } else {
+    e = launch_pdl(rank_kernel, dim3((unsigned)chunks), dim3(kChunk), cnt, a.st, a.ids, A, a.E, t);
+    if (e == cudaSuccess)
+      e = launch_pdl(place_kernel, dim3(1), dim3(1024), 0, a.st, t, a.E, chunks, bt_gu, bt_d);
+    auto scatter = a.dt == AWQ_DTYPE_F16 ? scatter_kernel<AWQ_DTYPE_F16> : scatter_kernel<AWQ_DTYPE_BF16>;
+    blocks = (warps + 7) / 8;
+    if (e == cudaSuccess)
+      e = launch_pdl(scatter, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, a.st, a.x, a.ids, a.M, a.E,
+                     a.topk, a.K, SW, t, ws + l.xc, xs);
+  }
   if (e != cudaSuccess) return AWQ_ERR_CUDA;
   W8Args g;
   g.groups = a.E;
@@ -284,6 +360,7 @@ awq_status moe_launch(const MoeArgs& a) {
   down.bt = bt_d;
   down.y = ws + l.d;
   down.dt = AWQ_DTYPE_F32;
+  down.plan_ready = true;  // the first product waits for the plan before it lets the second start
   st = w8a8_launch(down);
   if (st != AWQ_OK) return st;
   blocks = ((long long)a.M * ((a.N + 3) / 4) + 255) / 256;

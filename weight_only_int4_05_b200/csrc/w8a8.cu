@@ -18,8 +18,13 @@
 // its half of the accumulator, so each byte of x brought to an SM serves 256 rows.
 // Few tokens (splits > 1): a cluster shares one tile, each CTA a part of K; the partial sums meet in shared memory
 // (each CTA finishes some of the tokens, summing the parts in rank order), so there is no workspace and no counter.
+// At most 16 tokens (XQ): x comes as 16-bit values and the epilogue warps, idle until the tile's products are done,
+// quantize it into the ring, each CTA the part of K that it needs, so a decode step has no quantizer launch in front of it;
+// the codes and scales are those of fp8_quantize, bit for bit.
 // Every mbarrier wait is bounded; a timeout is recorded in the status word, the CTA drains its copies and MMAs, frees
 // its tensor memory and exits.
+#include <type_traits>
+
 #include "fp8.cuh"
 #include "w8a8.cuh"
 
@@ -30,8 +35,11 @@ namespace {
 constexpr int kTileW = 128;        // weight rows per accumulator and CTA
 constexpr int kBlkBytes = 128;     // bytes of K per k-block: one swizzle row, one scale block
 constexpr int kEpiGroups = 2;      // epilogue warpgroups
+constexpr int kXqMost = 16;        // tokens up to which the epilogue warps quantize x: 8 warps of 2 rows
+constexpr int kHalfMost = 32;      // tokens per tile up to which a CTA takes half an SM's shared memory
 constexpr int kW8Threads = 128 + 128 * kEpiGroups;
 constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on sm_100
+constexpr int kW8HalfSmem = 115712;  // two blocks per SM (1 KB of each block's share is the system's)
 #ifndef AWQ_W8_PAIR_BT
 #define AWQ_W8_PAIR_BT 128
 #endif
@@ -41,6 +49,8 @@ constexpr int kSfTmem = 2;         // and in tensor memory
 struct W8Params {
   const uint32_t* ws;  // scale words of w and x, SW per row
   const uint32_t* xs;
+  const uint16_t* x;   // XQ: x itself, [xrows][K] of type xdt
+  int K, xdt, plan_ready;
   void* y;
   uint8_t* hc;
   uint8_t* hs;
@@ -145,6 +155,7 @@ __device__ __forceinline__ void w8_silu_quant(const W8Params& p, const W8Tile& t
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
+    if (c + i >= t.rows) break;  // uniform
     h[i] = n < p.N ? w8_silu(a[i]) * b[i] : 0.f;
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h[i])));
     if (lane == i) mine = m;
@@ -155,18 +166,101 @@ __device__ __forceinline__ void w8_silu_quant(const W8Params& p, const W8Tile& t
   uint8_t* hs = p.hs + (size_t)(t.t0 + c) * (p.SWh * 4) + t.n0 / kFp8Block;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
+    if (c + i >= t.rows) break;
     const uint32_t s = fp8_scale_byte(max(max(buf[i], buf[16 + i]), max(buf[32 + i], buf[48 + i])));
-    if (c + i < t.rows && n < p.N) {
+    if (n < p.N) {
       hc[(size_t)i * p.N] = (uint8_t)e4m3x2(h[i] * fp8_inv_scale(s), 0.f);
       if (row == 0) hs[i * (p.SWh * 4)] = (uint8_t)s;
     }
   }
 }
 
+// One tile's x into the ring (XQ): warp xw takes token rows 2 xw and 2 xw + 1, half a warp per row, 8 values per lane and
+// k-block.  Four k-blocks (one word of scales) go at a time, the loads of the next four behind them.
+struct XqState {
+  int s = 0, cs = 0;            // ring stage and scale slot
+  unsigned phase = 1, cphase = 1;
+};
+template <int DT>
+__device__ __forceinline__ void w8_quantize_x(const W8Params& p, const W8Tile& t, uint8_t* xtile, uint8_t* sfx, int stage,
+                                              int slot, uint64_t* full, uint64_t* empty, uint64_t* sf_full,
+                                              uint64_t* sf_empty, volatile int* abort_flag, int kb0, int kb1, int xw,
+                                              int lane, XqState& st) {
+  const int r = xw * 2 + (lane >> 4);
+  const uint16_t* x = p.x + (size_t)(t.t0 + min(r, t.rows - 1)) * p.K + (lane & 15) * 8;
+  const int last = r < t.rows ? p.K - (lane & 15) * 8 : 0;  // columns from here on exist (in steps of 8)
+  uint4 v[4];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int kb = 4 * c + j;
+      v[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (kb >= kb0 && kb < kb1 && kb * kFp8Block < last) v[j] = *reinterpret_cast<const uint4*>(x + kb * kFp8Block);
+    }
+  };
+  const int c1 = (kb1 + 3) >> 2;
+  load(kb0 >> 2);
+  for (int c = kb0 >> 2; c < c1; ++c) {
+    uint2 q[4];
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      float f[8], m = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 pr = pair_to_f32<DT>(u[k]);
+        f[2 * k] = pr.x;
+        f[2 * k + 1] = pr.y;
+        m = fmaxf(m, fmaxf(fabsf(pr.x), fabsf(pr.y)));
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+      const uint32_t b = fp8_scale_byte(__float_as_uint(m));
+      const float inv = fp8_inv_scale(b);
+      word |= b << (8 * j);
+      q[j].x = e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
+      q[j].y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
+    }
+    if (c + 1 < c1) load(c + 1);
+    int s = st.s;
+    unsigned phase = st.phase;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (4 * c + j < kb0 || 4 * c + j >= kb1) continue;
+      if (!warp_wait(&empty[s], phase, p.status, abort_flag)) return;
+      // 128-byte swizzle: 16-byte piece n of row r stands at piece n ^ (r % 8)
+      *reinterpret_cast<uint2*>(xtile + s * stage + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8) = q[j];
+      if (++s == p.ST) {
+        s = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!warp_wait(&sf_empty[st.cs], st.cphase, p.status, abort_flag)) return;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(sfx + st.cs * slot + r * 16) = word;  // rows 0 .. 31: the first word of 16 bytes
+    fence_proxy_async_smem();
+    __syncwarp();
+    s = st.s;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (4 * c + j < kb0 || 4 * c + j >= kb1) continue;
+      if (lane == 0) mbar_arrive(&full[s]);
+      if (++s == p.ST) s = 0;
+    }
+    if (lane == 0) mbar_arrive(&sf_full[st.cs]);
+    st.s = s;
+    st.phase = phase;
+    if (++st.cs == kSf) {
+      st.cs = 0;
+      st.cphase ^= 1u;
+    }
+  }
+}
+
 }  // namespace
 
-template <int EPI, int CG>
-__global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_constant__ W8Maps maps, const W8Params p) {
+template <int EPI, int CG, bool XQ>
+__global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const __grid_constant__ W8Maps maps, const W8Params p) {
   constexpr int NA = kAtomsA<EPI>;
   extern __shared__ uint8_t w8_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w8_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -193,11 +287,11 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
   const int csize = CG == 2 ? 2 : p.splits;  // CTAs that share a tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ST; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], XQ ? 1 + 4 * kEpiGroups : 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kSf; ++s) {
-      mbar_init(&sf_full[s], CG);
+      mbar_init(&sf_full[s], XQ ? 1 + 4 * kEpiGroups : CG);
       mbar_init(&sf_empty[s], 1);
     }
     mbar_init(acc_full, 1);
@@ -208,12 +302,14 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.w);
-    prefetch_tensormap(&maps.x);
+    if (!XQ) prefetch_tensormap(&maps.x);
   }
   if (warp == 1) tmem_alloc_group<CG>(tmem_slot, (unsigned)p.tmem_cols);
   if (p.groups != 0) {
-    pdl_wait_prior_grids();
-    for (int i = threadIdx.x; i <= p.groups; i += kW8Threads) {
+    // The tables come from the kernel before this one, or (plan_ready) from one that it had waited for before it let this
+    // one start: then weights are fetched ahead of the wait as in the dense product.
+    if (!p.plan_ready) pdl_wait_prior_grids();
+    for (int i = threadIdx.x; i <= p.groups; i += (int)blockDim.x) {
       tabs[i] = p.tile_start[i];
       tabs[p.groups + 1 + i] = p.row_start[i];
     }
@@ -246,13 +342,14 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
       // In a pair both CTAs' copies count on the even CTA's barrier, which expects the bytes of both.
       const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : smem_u32(full);
       auto load_w = [&](const W8Tile& t, int kb, int s) {
-        if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(CG * stage));
+        if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(XQ ? NA * kTileW * kBlkBytes : CG * stage));
 #pragma unroll
         for (int a = 0; a < NA; ++a)
           tma_load_2d_group<CG>(base + s * stage + a * kTileW * kBlkBytes, &maps.w, kb * kBlkBytes, t.w0 + a * p.N,
                                 full0 + s * 8);
       };
       auto load_x = [&](const W8Tile& t, int kb, int s) {
+        if (XQ) return;
         tma_load_2d_group<CG>(base + s * stage + NA * kTileW * kBlkBytes, &maps.x, kb * kBlkBytes,
                               t.t0 + (CG == 2 ? rank * (p.BT / 2) : 0), full0 + s * 8);
       };
@@ -379,18 +476,18 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
               const int row = min(t.w0 + a * p.N + j * 32 + lane, p.wtotal - 1);
               va[a][j] = __ldg(p.ws + (size_t)row * p.SW + c);
             }
-          pdl_wait_prior_grids();  // x's scales come from the kernel before this one, the weight's do not
+          if (!XQ) pdl_wait_prior_grids();  // x's scales come from the kernel before this one, the weight's do not
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             vb[j] = 0;
-            if (j * 32 < p.BT) vb[j] = p.xs[(size_t)min(t.t0 + j * 32 + lane, p.xrows - 1) * p.SW + c];
+            if (!XQ && j * 32 < p.BT) vb[j] = p.xs[(size_t)min(t.t0 + j * 32 + lane, p.xrows - 1) * p.SW + c];
           }
           if (!(ok = warp_wait(&sf_empty[cs], phase, p.status, abort_flag))) break;
           // row i of a 512-byte atom: the words of rows i, i + 32, i + 64, i + 96
           uint4* dst = reinterpret_cast<uint4*>(sf + cs * slot);
 #pragma unroll
           for (int a = 0; a < NA; ++a) dst[a * 32 + lane] = make_uint4(va[a][0], va[a][1], va[a][2], va[a][3]);
-          dst[NA * 32 + lane] = make_uint4(vb[0], vb[1], vb[2], vb[3]);
+          if (!XQ) dst[NA * 32 + lane] = make_uint4(vb[0], vb[1], vb[2], vb[3]);
           if (p.BT > 128) dst[(NA + 1) * 32 + lane] = make_uint4(vb[4], vb[5], vb[6], vb[7]);
           fence_proxy_async_smem();
           __syncwarp();
@@ -415,6 +512,7 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
     const int shared = (NA * p.BT - p.acc_off + 15) / 16;  // chunks whose columns the next tile's accumulator takes
     uint32_t* my_amax = amax + wg * 128;
     int done = 0, turn = 0, decisions = 0;
+    XqState xq;
     // All epilogue warps take the same way out: one thread reads the flag for all.
     auto all_ok = [&]() {
       named_barrier_sync(1, 128 * kEpiGroups);
@@ -432,6 +530,14 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
     };
     for (int tile = first_tile; tile < tiles; tile += tile_step, ++done) {
       const W8Tile t = w8_tile<CG>(p, tabs, tile, rank);
+      if constexpr (XQ) {
+        auto quantize = [&](auto dt) {
+          w8_quantize_x<decltype(dt)::value>(p, t, smem + NA * kTileW * kBlkBytes, sf + NA * 512, stage, slot, full, empty,
+                                             sf_full, sf_empty, abort_flag, kb0, kb1, warp - 4, lane, xq);
+        };
+        if (p.xdt == AWQ_DTYPE_F16) quantize(std::integral_constant<int, AWQ_DTYPE_F16>{});
+        else quantize(std::integral_constant<int, AWQ_DTYPE_BF16>{});
+      }
       warp_wait(acc_full, (unsigned)(done & 1), p.status, abort_flag);
       if (!all_ok()) break;
       tc_fence_after_sync();
@@ -479,28 +585,39 @@ __global__ void __launch_bounds__(kW8Threads, 1) w8a8_kernel(const __grid_consta
         for (int j = 0; j < 16; ++j) part[(c + j) * kTileW + row] = __uint_as_float(v[j]);
       }
       release();
-      if (lane == 0)
-        for (int r = 0; r < p.splits; ++r) mbar_arrive_cluster(cluster_addr(part_full, (uint32_t)r));
+      // one lane per CTA of the cluster: each arrival carries a release, and eight in a row would take microseconds
+      if (lane < p.splits) mbar_arrive_cluster(cluster_addr(part_full, (uint32_t)lane));
       warp_wait(part_full, (unsigned)(done & 1), p.status, abort_flag);
       if (!all_ok()) break;
       const int share = p.BT / p.splits;  // tokens per CTA, a multiple of 2
-      for (int c = rank * share + 2 * wg; c < (rank + 1) * share; c += 2 * kEpiGroups) {
-        if (c >= t.rows) break;  // uniform
-        float f[2] = {0.f, 0.f}, g[2] = {0.f, 0.f};
-        for (int r = 0; r < p.splits; ++r) {
-          const uint32_t src = cluster_addr(part + c * kTileW + row, (uint32_t)r);
+#pragma unroll 2
+      for (int c = rank * share + 2 * wg; c < min((rank + 1) * share, t.rows); c += 2 * kEpiGroups) {
+        float v[8][2], u[8][2];  // all parts in flight at once
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const uint32_t src = cluster_addr(part + c * kTileW + row, (uint32_t)min(r, p.splits - 1));
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            f[j] += ld_cluster_f32(src + j * kTileW * 4);
-            if (NA == 2) g[j] += ld_cluster_f32(src + (p.BT + j) * kTileW * 4);
+            v[r][j] = u[r][j] = 0.f;
+            if (r < p.splits) {
+              v[r][j] = ld_cluster_f32(src + j * kTileW * 4);
+              if (NA == 2) u[r][j] = ld_cluster_f32(src + (p.BT + j) * kTileW * 4);
+            }
           }
         }
+        float f[2] = {0.f, 0.f}, g[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            f[j] += v[r][j];
+            if (NA == 2) g[j] += u[r][j];
+          }
         if constexpr (EPI == kW8Store) w8_store<2>(p, t, row, c, f);
         else w8_silu_quant<2>(p, t, row, c, f, g, my_amax, turn, 2 + wg);
       }
       __syncwarp();
-      if (lane == 0)
-        for (int r = 0; r < p.splits; ++r) mbar_arrive_cluster(cluster_addr(part_free, (uint32_t)r));
+      if (lane < p.splits) mbar_arrive_cluster(cluster_addr(part_free, (uint32_t)lane));
     }
   }
   tc_fence_before_sync();
@@ -544,13 +661,13 @@ bool encode_codes(EncodeTiledFn encode, CUtensorMap* map, const uint8_t* p, long
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI, int CG>
+template <int EPI, int CG, bool XQ>
 cudaError_t launch_one(const W8Maps& maps, const W8Params& p, int grid, int smem, cudaStream_t st) {
   static bool ready[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(w8a8_kernel<EPI, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
+    const cudaError_t e = cudaFuncSetAttribute(w8a8_kernel<EPI, CG, XQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
@@ -568,10 +685,12 @@ cudaError_t launch_one(const W8Maps& maps, const W8Params& p, int grid, int smem
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = attr[1].val.clusterDim.x > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, w8a8_kernel<EPI, CG>, maps, p);
+  return cudaLaunchKernelEx(&cfg, w8a8_kernel<EPI, CG, XQ>, maps, p);
 }
 
 }  // namespace
+
+bool w8a8_quantizes(int tokens) { return tokens <= kXqMost; }
 
 int w8a8_grouped_bt(long long rows, int groups, int epi) {
   const long long used = rows < groups ? rows : groups;
@@ -594,6 +713,7 @@ awq_status w8a8_launch(const W8Args& a) {
   p.hs = a.hs;
   p.row_start = a.row_start;
   p.tile_start = a.tile_start;
+  p.plan_ready = a.plan_ready;
   p.status = a.status;
   p.xrows = a.xrows;
   p.wrows = a.N * atoms;
@@ -615,33 +735,45 @@ awq_status w8a8_launch(const W8Args& a) {
   const long long bound = tt * p.n_tiles;
   if (bound > 0x7FFFFFFF || wtotal > 0x7FFFFFFF) return AWQ_ERR_UNSUPPORTED;
   const int sms = num_sms();
+  // Few tokens: two CTAs per SM, so that the next kernel's weights are under way while this one ends, and K split over a
+  // cluster until the tiles fill both halves.
+  const bool half = cg == 1 && p.BT <= kHalfMost;
+  const int slots = half ? 2 * sms : sms;
   p.splits = 1;
-  if (cg == 1 && p.BT <= 32)
-    while (p.splits < 8 && bound * p.splits * 2 <= sms && p.KB >= p.splits * 4) p.splits *= 2;
+  if (half)
+    while (p.splits < 8 && bound * p.splits * 2 <= slots && p.KB >= p.splits * 4) p.splits *= 2;
   const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
   const int part = p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
   const int rest = 1024 + kSf * slot + part + 512 + 64 + kEpiGroups * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
-  p.ST = (kW8Smem - rest) / stage;
+  p.ST = ((half ? kW8HalfSmem : kW8Smem) - rest) / stage;
   if (p.ST > 12) p.ST = 12;
+  if (p.ST < 2) return AWQ_ERR_UNSUPPORTED;
   const int sfc = kSfTmem * w8_sf_cols(atoms, p.BT), acc = atoms * p.BT;
   p.acc_off = acc < 512 - sfc - acc ? acc : 512 - sfc - acc;
   p.tmem_cols = 32;
   while (p.tmem_cols < p.acc_off + acc + sfc) p.tmem_cols <<= 1;
-  if (p.ST < 2 || p.tmem_cols > 512) return AWQ_ERR_UNSUPPORTED;
   p.idesc = umma_idesc_mxf8(kTileW * cg, p.BT);
   W8Maps maps;
-  if (!encode_codes(encode, &maps.w, a.wc, wtotal, a.K, kTileW) ||
-      !encode_codes(encode, &maps.x, a.xc, a.xrows, a.K, p.BT / cg))
+  if (!encode_codes(encode, &maps.w, a.wc, wtotal, a.K, kTileW)) return AWQ_ERR_CUDA;
+  const bool xq = a.x != nullptr;
+  if (xq) {
+    if (cg != 1 || a.groups || p.BT > kXqMost || p.ST < 5) return AWQ_ERR_UNSUPPORTED;  // 4 k-blocks are quantized at a time
+    p.x = a.x;
+    p.K = a.K;
+    p.xdt = a.xdt;
+  } else if (!encode_codes(encode, &maps.x, a.xc, a.xrows, a.K, p.BT / cg)) {
     return AWQ_ERR_CUDA;
+  }
   const int csize = cg == 2 ? 2 : p.splits;
-  const long long most_units = sms / csize;
+  const long long most_units = slots / csize;
   const int grid = (int)(bound < most_units ? bound : most_units) * csize;
   const int smem = rest + p.ST * stage;
-  const cudaError_t e = a.epi == kW8SiluQuant
-                            ? (cg == 2 ? launch_one<kW8SiluQuant, 2>(maps, p, grid, smem, a.st)
-                                       : launch_one<kW8SiluQuant, 1>(maps, p, grid, smem, a.st))
-                            : (cg == 2 ? launch_one<kW8Store, 2>(maps, p, grid, smem, a.st)
-                                       : launch_one<kW8Store, 1>(maps, p, grid, smem, a.st));
+  const bool quant = a.epi == kW8SiluQuant;
+  const cudaError_t e = xq ? launch_one<kW8Store, 1, true>(maps, p, grid, smem, a.st)
+                        : cg == 2 ? (quant ? launch_one<kW8SiluQuant, 2, false>(maps, p, grid, smem, a.st)
+                                           : launch_one<kW8Store, 2, false>(maps, p, grid, smem, a.st))
+                                  : (quant ? launch_one<kW8SiluQuant, 1, false>(maps, p, grid, smem, a.st)
+                                           : launch_one<kW8Store, 1, false>(maps, p, grid, smem, a.st));
   return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;
 }
 

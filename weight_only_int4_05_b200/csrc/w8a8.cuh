@@ -13,6 +13,8 @@ enum W8Epilogue { kW8Store = 0, kW8SiluQuant = 1 };
 struct W8Args {
   const uint8_t* xc = nullptr;   // codes and scales of x
   const uint8_t* xs = nullptr;
+  const uint16_t* x = nullptr;   // dense, instead of xc and xs where w8a8_quantizes(xrows): x itself, 16-bit of type xdt
+  int xdt = 0;
   int xrows = 0;                 // rows of x that exist (grouped: an upper bound)
   const uint8_t* wc = nullptr;   // codes and scales of w
   const uint8_t* wsc = nullptr;
@@ -21,6 +23,7 @@ struct W8Args {
   const int* row_start = nullptr;
   const int* tile_start = nullptr;
   int bt = 0;                    // grouped: token tile (w8a8_grouped_bt)
+  bool plan_ready = false;       // grouped: the kernel before this one on the stream has itself waited for the tables' kernel
   int epi = kW8Store;
   void* y = nullptr;             // kW8Store: [rows][N] of type dt
   int dt = 0;
@@ -29,6 +32,7 @@ struct W8Args {
   unsigned* status = nullptr;
   cudaStream_t st = nullptr;
 };
+bool w8a8_quantizes(int tokens);  // whether the dense product takes `tokens` rows of 16-bit x
 int w8a8_grouped_bt(long long rows, int groups, int epi);  // token tile for `rows` rows spread over `groups` groups
 awq_status w8a8_launch(const W8Args& a);
 awq_status fp8_quantize_launch(const void* x, int dt, int R, int K, uint8_t* codes, uint8_t* scales, cudaStream_t st,

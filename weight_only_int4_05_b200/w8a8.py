@@ -81,14 +81,17 @@ def _output(out: Optional[torch.Tensor], M: int, N: int, dtype: torch.dtype, dev
     return out
 
 
-def _scratch(fn: str, need: int, workspace: Optional[torch.Tensor], device: torch.device) -> torch.Tensor:
+def _scratch(fn: str, need: int, workspace: Optional[torch.Tensor], device: torch.device):
+    """The scratch tensor of a call, its address and bytes."""
     if need == 2**64 - 1:
         raise AwqError(fn, 1)
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def fp8_quantize(x: torch.Tensor, out: Optional[Fp8Matrix] = None) -> Fp8Matrix:
@@ -143,9 +146,9 @@ def w8a8_linear(x: Union[torch.Tensor, Fp8Matrix], w: Fp8Matrix, out: Optional[t
         _run("w8a8_gemm", lib.w8a8_gemm, dev, (x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(),
                                                w.scales.data_ptr(), y.data_ptr(), _DTYPES[dtype], M, N, K, stream))
         return y
-    ws = _scratch("w8a8_linear", w8a8_workspace_bytes(M, N, K), workspace, dev)
+    ws, at, size = _scratch("w8a8_linear", w8a8_workspace_bytes(M, N, K), workspace, dev)
     _run("w8a8_linear", lib.w8a8_linear, dev, (x.data_ptr(), _DTYPES[dtype], w.codes.data_ptr(), w.scales.data_ptr(),
-                                               y.data_ptr(), M, N, K, ws.data_ptr(), ws.nbytes, stream))
+                                               y.data_ptr(), M, N, K, at, size, stream))
     return y
 
 
@@ -195,10 +198,10 @@ def w8a8_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up:
     if gk != K or de != E or 2 * I != two_i:
         raise ValueError(f"gate_up {tuple(gate_up.codes.shape)} and down {tuple(down.codes.shape)} do not match x's K={K}")
     y = _output(out, M, N, x.dtype, dev)
-    ws = _scratch("w8a8_moe", w8a8_moe_workspace_bytes(M, E, topk, K, I, N), workspace, dev)
+    ws, at, size = _scratch("w8a8_moe", w8a8_moe_workspace_bytes(M, E, topk, K, I, N), workspace, dev)
     lib, stream = _library(dev)
     _run("w8a8_moe", lib.w8a8_moe, dev, (
         x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(), weights.data_ptr(), gate_up.codes.data_ptr(),
         gate_up.scales.data_ptr(), down.codes.data_ptr(), down.scales.data_ptr(), y.data_ptr(), M, E, topk, K, I, N,
-        ws.data_ptr(), ws.nbytes, stream))
+        at, size, stream))
     return y
