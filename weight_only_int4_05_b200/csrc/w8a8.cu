@@ -23,6 +23,8 @@
 // the codes and scales are those of fp8_quantize, bit for bit.
 // Every mbarrier wait is bounded; a timeout is recorded in the status word, the CTA drains its copies and MMAs, frees
 // its tensor memory and exits.
+#include <math.h>
+
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -41,7 +43,7 @@ constexpr int kW8Threads = 128 + 128 * kEpiGroups;
 constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on sm_100
 constexpr int kW8HalfSmem = 115712;  // two blocks per SM (1 KB of each block's share is the system's)
 #ifndef AWQ_W8_PAIR_BT
-#define AWQ_W8_PAIR_BT 128
+#define AWQ_W8_PAIR_BT 64
 #endif
 constexpr int kSf = 4;             // scale slots (4 k-blocks each) in shared memory
 constexpr int kSfTmem = 2;         // and in tensor memory
@@ -118,6 +120,25 @@ __device__ __forceinline__ float w8_silu(float a) {
   return __fdividef(a, 1.0f + e);
 }
 
+// W columns of this warp's 32 lanes of tensor memory; the registers hold them after tmem_wait_ld alone.
+template <int W>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[W]) {
+  if constexpr (W == 16) {
+    tmem_ld_32x32b_x16(taddr, v);
+  } else {
+    static_assert(W == 4, "4 or 16 columns");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(taddr)
+                 : "memory");
+  }
+}
+template <int W>
+__device__ __forceinline__ void tmem_cols_f32(const uint32_t (&v)[W], float (&f)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) f[i] = __uint_as_float(v[i]);
+}
+
 // Outputs of weight row n0 + row for the W tokens from column c of the tile on.
 template <int W, typename T, typename F>
 __device__ __forceinline__ void w8_store_as(const W8Params& p, const W8Tile& t, int row, int c, const float (&f)[W], F to) {
@@ -155,7 +176,6 @@ __device__ __forceinline__ void w8_silu_quant(const W8Params& p, const W8Tile& t
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    if (c + i >= t.rows) break;  // uniform
     h[i] = n < p.N ? w8_silu(a[i]) * b[i] : 0.f;
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h[i])));
     if (lane == i) mine = m;
@@ -166,9 +186,8 @@ __device__ __forceinline__ void w8_silu_quant(const W8Params& p, const W8Tile& t
   uint8_t* hs = p.hs + (size_t)(t.t0 + c) * (p.SWh * 4) + t.n0 / kFp8Block;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    if (c + i >= t.rows) break;
     const uint32_t s = fp8_scale_byte(max(max(buf[i], buf[16 + i]), max(buf[32 + i], buf[48 + i])));
-    if (n < p.N) {
+    if (c + i < t.rows && n < p.N) {
       hc[(size_t)i * p.N] = (uint8_t)e4m3x2(h[i] * fp8_inv_scale(s), 0.f);
       if (row == 0) hs[i * (p.SWh * 4)] = (uint8_t)s;
     }
@@ -272,8 +291,8 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
   uint64_t* sf_full = empty + p.ST;
   uint64_t* sf_empty = sf_full + kSf;
   uint64_t* acc_full = sf_empty + kSf;
-  uint64_t* acc_free = acc_full + 1;
-  uint64_t* drain = acc_free + 1;
+  uint64_t* acc_free = acc_full + 2;  // one of each per accumulator: the products may run two tiles ahead of the epilogue
+  uint64_t* drain = acc_free + 2;
   uint64_t* part_full = drain + 1;
   uint64_t* part_free = part_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_free + 1);
@@ -294,8 +313,10 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
       mbar_init(&sf_full[s], XQ ? 1 + 4 * kEpiGroups : CG);
       mbar_init(&sf_empty[s], 1);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_free, 4 * kEpiGroups * CG);
+    mbar_init(&acc_full[0], 1);
+    mbar_init(&acc_full[1], 1);
+    mbar_init(&acc_free[0], 4 * kEpiGroups * CG);
+    mbar_init(&acc_free[1], 4 * kEpiGroups * CG);
     mbar_init(drain, 1);
     mbar_init(part_full, 4 * kEpiGroups * p.splits);
     mbar_init(part_free, 4 * kEpiGroups * p.splits);
@@ -326,6 +347,7 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
   const int kb0 = (int)((long long)p.KB * srank / p.splits), kb1 = (int)((long long)p.KB * (srank + 1) / p.splits);
   const uint32_t sf_tmem = tmem + (uint32_t)(p.acc_off + NA * p.BT);
   const uint32_t sf_cols = (uint32_t)w8_sf_cols(NA, p.BT);
+  const bool apart = p.acc_off >= NA * p.BT;  // the two accumulators share no columns
 
   if (warp == 0) {
     if (lane == 0) {
@@ -403,7 +425,13 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
       bool ok = true;
       const uint32_t base = smem_u32(smem), sfbase = smem_u32(sf);
       for (int tile = first_tile; tile < tiles && ok; tile += tile_step, ++done) {
-        if (done > 0 && !warp_wait(acc_free, (unsigned)((done - 1) & 1), p.status, abort_flag)) break;
+        // The accumulator is free once the epilogue has read the tile that it held last, two tiles ago (a barrier for each);
+        // where the two share columns, once it has read those of the tile before this one (the first barrier).
+        if (apart ? done > 1 : done > 0) {
+          const bool freed = apart ? warp_wait(&acc_free[done & 1], (unsigned)((done >> 1) - 1) & 1u, p.status, abort_flag)
+                                   : warp_wait(&acc_free[0], (unsigned)(done - 1) & 1u, p.status, abort_flag);
+          if (!freed) break;
+        }
         tc_fence_after_sync();
         const uint32_t acc = tmem + ((done & 1) ? (uint32_t)p.acc_off : 0u);
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -439,7 +467,7 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
                               k > 0 || kb > kb0);
             umma_commit_group<CG>(&empty[s]);
             if (last) umma_commit_group<CG>(&sf_empty[cs]);
-            if (kb == kb1 - 1) umma_commit_group<CG>(acc_full);
+            if (kb == kb1 - 1) umma_commit_group<CG>(&acc_full[done & 1]);
           }
           __syncwarp();
           if (++s == p.ST) {
@@ -508,8 +536,9 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
     const int q = warp & 3, row = 32 * q + lane;  // tensor-memory lanes 32 q .. 32 q + 31 are this warp's weight rows
     const int wg = (warp - 4) >> 2;
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
-    const int chunks = p.BT / 16;
-    const int shared = (NA * p.BT - p.acc_off + 15) / 16;  // chunks whose columns the next tile's accumulator takes
+    constexpr int CW = CG == 2 ? 16 : 4;  // tokens at a time: few where a tile has few, so that the code stays short
+    const int chunks = p.BT / CW;
+    const int shared = (NA * p.BT - p.acc_off + CW - 1) / CW;  // chunks whose columns the next tile's accumulator takes
     uint32_t* my_amax = amax + wg * 128;
     int done = 0, turn = 0, decisions = 0;
     XqState xq;
@@ -524,8 +553,9 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2) mbar_arrive_cluster(cluster_addr(acc_free, 0));
-        else mbar_arrive(acc_free);
+        uint64_t* bar = &acc_free[apart ? done & 1 : 0];
+        if (CG == 2) mbar_arrive_cluster(cluster_addr(bar, 0));
+        else mbar_arrive(bar);
       }
     };
     for (int tile = first_tile; tile < tiles; tile += tile_step, ++done) {
@@ -538,38 +568,35 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
         if (p.xdt == AWQ_DTYPE_F16) quantize(std::integral_constant<int, AWQ_DTYPE_F16>{});
         else quantize(std::integral_constant<int, AWQ_DTYPE_BF16>{});
       }
-      warp_wait(acc_full, (unsigned)(done & 1), p.status, abort_flag);
+      warp_wait(&acc_full[done & 1], (unsigned)(done >> 1) & 1u, p.status, abort_flag);
       if (!all_ok()) break;
       tc_fence_after_sync();
       const int buf = done & 1;
       const uint32_t acc = tq + (buf ? (uint32_t)p.acc_off : 0u);
       if (p.splits == 1) {
         bool held = true;
-        if (wg >= shared) {
+        if (!apart && wg >= shared) {
           release();
           held = false;
         }
         for (int i = wg; i < chunks; i += kEpiGroups) {
-          const int c = 16 * (buf ? i : chunks - 1 - i);  // the shared columns are the first buffer's last, the second's first
-          uint32_t v[16], u[16];
-          tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
-          if (NA == 2) tmem_ld_32x32b_x16(acc + (uint32_t)(p.BT + c), u);
+          const int c = CW * (buf ? i : chunks - 1 - i);  // the shared columns are the first buffer's last, the second's first
+          uint32_t v[CW], u[CW];
+          tmem_ld_cols<CW>(acc + (uint32_t)c, v);
+          if (NA == 2) tmem_ld_cols<CW>(acc + (uint32_t)(p.BT + c), u);
           tmem_wait_ld();
-          if (held && i + kEpiGroups >= shared) {
+          if (held && (apart ? i + kEpiGroups >= chunks : i + kEpiGroups >= shared)) {
             release();
             held = false;
           }
           if (c >= t.rows) continue;  // uniform: no token of this chunk exists
-          float f[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+          float f[CW], g[CW];
+          tmem_cols_f32<CW>(v, f);
           if constexpr (EPI == kW8Store) {
-            w8_store<16>(p, t, row, c, f);
+            w8_store<CW>(p, t, row, c, f);
           } else {
-            float g[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) g[j] = __uint_as_float(u[j]);
-            w8_silu_quant<16>(p, t, row, c, f, g, my_amax, turn, 2 + wg);
+            tmem_cols_f32<CW>(u, g);
+            w8_silu_quant<CW>(p, t, row, c, f, g, my_amax, turn, 2 + wg);
           }
         }
         if (held) release();
@@ -692,13 +719,24 @@ cudaError_t launch_one(const W8Maps& maps, const W8Params& p, int grid, int smem
 
 bool w8a8_quantizes(int tokens) { return tokens <= kXqMost; }
 
+// The token tile of a grouped product.  Rows spread over the groups at random are about `avg` per group, give or take the
+// square root; a tile costs its columns, full or not, and about 32 columns' time for its weights.
 int w8a8_grouped_bt(long long rows, int groups, int epi) {
   const long long used = rows < groups ? rows : groups;
-  const long long avg = (rows + used - 1) / used;
+  const double avg = (double)rows / (double)used, dev = 1.2 * sqrt(avg);
   const int most = epi == kW8SiluQuant ? 128 : 256;
-  int bt = 16;
-  while (bt < avg && bt < most) bt <<= 1;
-  return bt;
+  int best = 16;
+  double least = 1e30;
+  for (int bt = 16; bt <= most; bt += 16) {
+    double tiles = 0.0;
+    for (int k = -1; k <= 1; ++k) tiles += ceil(fmax(avg + k * dev, 1.0) / bt) / 3.0;
+    const double cost = tiles * (bt + 32);
+    if (cost < least) {
+      least = cost;
+      best = bt;
+    }
+  }
+  return best;
 }
 
 awq_status w8a8_launch(const W8Args& a) {
