@@ -404,7 +404,7 @@ size_t fp8_scale_bytes(int R, int K);
 /*
  * fp8_quantize -- a 16-bit matrix (a weight, or activations) to the 8-bit format above.
  *   d_x [R][K] of dtype, device;  d_codes [R][K], d_scales fp8_scale_bytes(R, K), device, written.
- * Errors: AWQ_ERR_UNSUPPORTED (dtype), AWQ_ERR_INVALID_ARG (R < 1, K % 16 != 0, NULL), AWQ_ERR_MISALIGNED, AWQ_ERR_CUDA.
+ * Errors: AWQ_ERR_UNSUPPORTED (dtype), AWQ_ERR_INVALID_ARG (R < 1 or above 2^30, K % 16 != 0, NULL), AWQ_ERR_MISALIGNED, AWQ_ERR_CUDA.
  */
 awq_status fp8_quantize(const void* d_x, int dtype, int R, int K, uint8_t* d_codes, uint8_t* d_scales,
                         awq_stream_t stream);

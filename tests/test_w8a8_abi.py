@@ -35,6 +35,7 @@ def test_quantize_checks(L):
     assert L.fp8_quantize(F, 3, 4, 512, F, F, None) == 2
     assert L.fp8_quantize(F, 0, 4, 512, F, F, None) == 2
     assert L.fp8_quantize(F, 1, 0, 512, F, F, None) == 1
+    assert L.fp8_quantize(F, 1, (1 << 30) + 1, 16, F, F, None) == 1
     assert L.fp8_quantize(F, 1, 4, 504, F, F, None) == 1
     assert L.fp8_quantize(None, 1, 4, 512, F, F, None) == 1
     assert L.fp8_quantize(F, 1, 4, 512, F, None, None) == 1

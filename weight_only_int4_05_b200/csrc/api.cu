@@ -355,14 +355,14 @@ static bool dtype16(int dt) { return dt == AWQ_DTYPE_F16 || dt == AWQ_DTYPE_BF16
 static bool size_ok(int v, int most, int multiple) { return v >= 1 && v <= most && v % multiple == 0; }
 
 size_t fp8_scale_bytes(int R, int K) {
-  if (R < 1 || !size_ok(K, kMaxK, 16)) return SIZE_MAX;
+  if (!size_ok(R, 1 << 30, 1) || !size_ok(K, kMaxK, 16)) return SIZE_MAX;
   return (size_t)R * (size_t)fp8_scale_cols(K);
 }
 
 awq_status fp8_quantize(const void* d_x, int dtype, int R, int K, uint8_t* d_codes, uint8_t* d_scales,
                         awq_stream_t stream) {
   if (!dtype16(dtype)) return AWQ_ERR_UNSUPPORTED;
-  if (R < 1 || !size_ok(K, kMaxK, 16) || !d_x || !d_codes || !d_scales) return AWQ_ERR_INVALID_ARG;
+  if (!size_ok(R, 1 << 30, 1) || !size_ok(K, kMaxK, 16) || !d_x || !d_codes || !d_scales) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(d_x) || !aligned16(d_codes) || !aligned16(d_scales)) return AWQ_ERR_MISALIGNED;
   return fp8_quantize_launch(d_x, dtype, R, K, d_codes, d_scales, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -10,24 +10,37 @@ namespace awq {
 // One warp takes 512 columns of one row: lane l holds the 8 columns at 8 l of each half (two 16-byte loads), so the
 // 16 lanes of a half warp share a block of 128 and its maximum takes four shuffles; the four scale bytes are one word.
 template <int DT, bool EARLY>
-__global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* x, int R, int K, int SW,
-                                                           uint8_t* codes, uint32_t* scales) {
+__global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* x, int R, int K, int SW, uint8_t* codes,
+                                                           uint32_t* scales) {
   if (EARLY) pdl_launch_dependents();
   pdl_wait_prior_grids();
   const int lane = threadIdx.x & 31;
-  const long long items = (long long)R * SW;
-  const long long step = (long long)gridDim.x * (blockDim.x >> 5);
-  for (long long it = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += step) {
-    const long long row = it / SW;
-    const int w = (int)(it - row * SW);
+  const int step = (int)gridDim.x * 8, first = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5);
+  const int step_row = step / SW, step_w = step - step_row * SW;  // one division each here instead of one per item
+  int row = first / SW, w = first - row * SW;
+  const int blocks = fp8_blocks(K);
+  uint4 v[2];
+  auto load = [&](int r, int c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = c * 512 + h * 256 + lane * 8;
+      v[h] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < R && k < K) v[h] = ldg_stream(x + (size_t)r * K + k);
+    }
+  };
+  load(row, w);
+  while (row < R) {
+    const uint4 now[2] = {v[0], v[1]};
+    int next_row = row + step_row, next_w = w + step_w;
+    if (next_w >= SW) {
+      next_w -= SW;
+      ++next_row;
+    }
+    load(next_row, next_w);  // the next item's values are on their way while this one is quantized
     uint32_t word = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = w * 512 + h * 256 + lane * 8;
-      const bool in = k < K;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (in) v = ldg_stream(x + row * K + k);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t u[4] = {now[h].x, now[h].y, now[h].z, now[h].w};
       float f[8];
       float m = 0.f;
 #pragma unroll
@@ -41,18 +54,21 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* x, in
       for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
       const uint32_t b = fp8_scale_byte(__float_as_uint(m));
       const float inv = fp8_inv_scale(b);
-      if (in) {
+      const int k = w * 512 + h * 256 + lane * 8;
+      if (k < K) {
         uint2 c;
         c.x = e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16);
         c.y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
-        *reinterpret_cast<uint2*>(codes + row * K + k) = c;
+        *reinterpret_cast<uint2*>(codes + (size_t)row * K + k) = c;
       }
       const int blk = w * 4 + h * 2;
       const uint32_t other = __shfl_sync(0xFFFFFFFFu, b, 16);  // the second block of this half, for lane 0
-      word |= (blk < fp8_blocks(K) ? b : 127u) << (16 * h);
-      word |= (blk + 1 < fp8_blocks(K) ? other : 127u) << (16 * h + 8);
+      word |= (blk < blocks ? b : 127u) << (16 * h);
+      word |= (blk + 1 < blocks ? other : 127u) << (16 * h + 8);
     }
-    if (lane == 0) scales[row * SW + w] = word;
+    if (lane == 0) scales[(size_t)row * SW + w] = word;
+    row = next_row;
+    w = next_w;
   }
 }
 

@@ -42,9 +42,7 @@ constexpr int kHalfMost = 32;      // tokens per tile up to which a CTA takes ha
 constexpr int kW8Threads = 128 + 128 * kEpiGroups;
 constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on sm_100
 constexpr int kW8HalfSmem = 115712;  // two blocks per SM (1 KB of each block's share is the system's)
-#ifndef AWQ_W8_PAIR_BT
-#define AWQ_W8_PAIR_BT 64
-#endif
+constexpr int kPairLeast = 64;     // tokens per tile from which two CTAs work on it together
 constexpr int kSf = 4;             // scale slots (4 k-blocks each) in shared memory
 constexpr int kSfTmem = 2;         // and in tensor memory
 
@@ -162,6 +160,87 @@ __device__ __forceinline__ void w8_store(const W8Params& p, const W8Tile& t, int
     w8_store_as<W, __half>(p, t, row, c, f, [](float v) { return __float2half_rn(v); });
   else
     w8_store_as<W, __nv_bfloat16>(p, t, row, c, f, [](float v) { return __float2bfloat16_rn(v); });
+}
+
+// The same through shared memory, for the pair's large tiles: 16 tokens of the 128 rows are turned round, so that a warp
+// writes whole runs of 128 outputs of 4 tokens (256 or 512 contiguous bytes) where it wrote 16 runs of 32; for outputs whose
+// row length is a multiple of 4.  `turned` is the warpgroup's [16][128]; v gets the 4 outputs of tokens 4 q .. 4 q + 3 from
+// output 4 lane on.
+__device__ __forceinline__ void w8_turn(const float (&f)[16], int row, uint32_t turned, int bar, float4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(turned + (uint32_t)(i * kTileW + row) * 4), "f"(f[i]) : "memory");
+  named_barrier_sync(bar, 128);
+  const uint32_t src = turned + (uint32_t)((row >> 5) * (4 * kTileW) + (row & 31) * 4) * 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[j].x), "=f"(v[j].y), "=f"(v[j].z), "=f"(v[j].w)
+                 : "r"(src + j * kTileW * 4)
+                 : "memory");
+  named_barrier_sync(bar, 128);
+}
+__device__ __forceinline__ void st_global_v2(void* p, uint32_t a, uint32_t b) {
+  asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void w8_put(float* y, float4 v) {
+  asm volatile("st.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(y), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void w8_put(__half* y, float4 v) {
+  st_global_v2(y, h2_as_u32(__floats2half2_rn(v.x, v.y)), h2_as_u32(__floats2half2_rn(v.z, v.w)));
+}
+__device__ __forceinline__ void w8_put(__nv_bfloat16* y, float4 v) {
+  __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  st_global_v2(y, *reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+}
+template <typename T>
+__device__ __forceinline__ void w8_store_turned_as(const W8Params& p, const W8Tile& t, int row, int c, const float4 (&v)[4]) {
+  const int n = t.n0 + (row & 31) * 4, first = c + (row >> 5) * 4, rows = t.rows - first;
+  if (n >= p.N) return;
+  T* y = static_cast<T*>(p.y) + (size_t)(t.t0 + first) * p.N + n;
+#pragma unroll
+  for (int j = 0; j < 4; ++j, y += p.N)
+    if (j < rows) w8_put(y, v[j]);
+}
+__device__ __forceinline__ void w8_store_turned(const W8Params& p, const W8Tile& t, int row, int c, const float (&f)[16],
+                                                uint32_t turned, int bar) {
+  float4 v[4];
+  w8_turn(f, row, turned, bar, v);
+  if (p.dt == AWQ_DTYPE_F32) w8_store_turned_as<float>(p, t, row, c, v);
+  else if (p.dt == AWQ_DTYPE_F16) w8_store_turned_as<__half>(p, t, row, c, v);
+  else w8_store_turned_as<__nv_bfloat16>(p, t, row, c, v);
+}
+
+// h = silu(a) b of 16 tokens, quantized, through shared memory as above: a warp holds the 128 channels of a token, one block
+// of the 8-bit format, 4 per lane.
+__device__ __forceinline__ void w8_silu_quant_turned(const W8Params& p, const W8Tile& t, int row, int c,
+                                                     const float (&a)[16], const float (&b)[16], uint32_t turned, int bar) {
+  const int lane = row & 31, n = t.n0 + lane * 4, first = c + (row >> 5) * 4, rows = t.rows - first;
+  float h[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) h[i] = w8_silu(a[i]) * b[i];
+  if (t.n0 + row >= p.N) {  // rows of another expert or of none
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = 0.f;
+  }
+  float4 v[4];
+  w8_turn(h, row, turned, bar, v);
+  uint32_t s[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float m = fmaxf(fmaxf(fabsf(v[j].x), fabsf(v[j].y)), fmaxf(fabsf(v[j].z), fabsf(v[j].w)));
+    s[j] = fp8_scale_byte(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m)));
+  }
+  uint8_t* hc = p.hc + (size_t)(t.t0 + first) * p.N + n;
+  uint8_t* hs = p.hs + (size_t)(t.t0 + first) * (p.SWh * 4) + t.n0 / kFp8Block;
+#pragma unroll
+  for (int j = 0; j < 4; ++j, hc += p.N, hs += p.SWh * 4) {
+    const float inv = fp8_inv_scale(s[j]);
+    const uint32_t q = e4m3x2(v[j].x * inv, v[j].y * inv) | (e4m3x2(v[j].z * inv, v[j].w * inv) << 16);
+    // N is a multiple of 16
+    if (j < rows && n < p.N) asm volatile("st.global.b32 [%0], %1;" ::"l"(hc), "r"(q) : "memory");
+    if (j < rows && lane == 0) asm volatile("st.global.b8 [%0], %1;" ::"l"(hs), "r"(s[j]) : "memory");
+  }
 }
 
 // h = silu(a) b of the same tokens, quantized: the 128 rows of the tile are one block of the 8-bit format, so its maximum
@@ -286,7 +365,8 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
   const int stage = w8_stage(NA, p.BT / CG), slot = w8_sf_slot(NA, p.BT);
   uint8_t* sf = smem + p.ST * stage;
   float* part = reinterpret_cast<float*>(sf + kSf * slot);  // splits > 1: [NA * BT][128] partial sums
-  uint64_t* full = reinterpret_cast<uint64_t*>(part + (p.splits > 1 ? NA * p.BT * kTileW : 0));
+  // a pair: [kEpiGroups][16][128], the epilogue's turning space in its place
+  uint64_t* full = reinterpret_cast<uint64_t*>(part + (CG == 2 ? kEpiGroups * 16 * kTileW : p.splits > 1 ? NA * p.BT * kTileW : 0));
   uint64_t* empty = full + p.ST;
   uint64_t* sf_full = empty + p.ST;
   uint64_t* sf_empty = sf_full + kSf;
@@ -592,11 +672,15 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
           if (c >= t.rows) continue;  // uniform: no token of this chunk exists
           float f[CW], g[CW];
           tmem_cols_f32<CW>(v, f);
-          if constexpr (EPI == kW8Store) {
-            w8_store<CW>(p, t, row, c, f);
+          if constexpr (EPI == kW8SiluQuant) tmem_cols_f32<CW>(u, g);
+          if constexpr (CG == 2) {
+            const uint32_t turned = smem_u32(part + wg * (16 * kTileW));
+            if constexpr (EPI == kW8SiluQuant) w8_silu_quant_turned(p, t, row, c, f, g, turned, 2 + wg);
+            else if ((p.N & 3) == 0) w8_store_turned(p, t, row, c, f, turned, 2 + wg);
+            else w8_store<CW>(p, t, row, c, f);
           } else {
-            tmem_cols_f32<CW>(u, g);
-            w8_silu_quant<CW>(p, t, row, c, f, g, my_amax, turn, 2 + wg);
+            if constexpr (EPI == kW8SiluQuant) w8_silu_quant<CW>(p, t, row, c, f, g, my_amax, turn, 2 + wg);
+            else w8_store<CW>(p, t, row, c, f);
           }
         }
         if (held) release();
@@ -717,6 +801,28 @@ cudaError_t launch_one(const W8Maps& maps, const W8Params& p, int grid, int smem
 
 }  // namespace
 
+// The token tile of the dense product.  Up to 32 tokens one tile; above, the tile whose waves over the SMs take the least
+// time by a count of cycles: per k-block the larger of the products (2 per token), of their issue (300) and of the operands'
+// way from L2 (64 bytes a cycle and SM), then the last tile's epilogue (30 per token) and a tile's start.
+int dense_bt(int M, int N, int KB, int sms) {
+  if (M <= kHalfMost) return (M + 15) / 16 * 16;
+  int best = 16;
+  double least = 1e30;
+  for (int bt = 48; bt <= 256; bt += 16) {
+    const int cg = bt >= kPairLeast ? 2 : 1;
+    const double tiles = (double)((M + bt - 1) / bt) * ((N + kTileW * cg - 1) / (kTileW * cg));
+    const double waves = ceil(tiles / (sms / cg));
+    const double block = fmax(fmax(2.0 * bt, 300.0), (kTileW + (double)bt / cg) * kBlkBytes / 64.0);
+    const double cost = waves * (KB * block + 1000.0) + 30.0 * bt;
+    if (cost < least) {
+      least = cost;
+      best = bt;
+    }
+    if (bt >= M) break;
+  }
+  return best;
+}
+
 bool w8a8_quantizes(int tokens) { return tokens <= kXqMost; }
 
 // The token tile of a grouped product.  Rows spread over the groups at random are about `avg` per group, give or take the
@@ -761,18 +867,17 @@ awq_status w8a8_launch(const W8Args& a) {
   p.SWh = fp8_scale_cols(a.N) / 4;
   p.groups = a.groups;
   p.dt = a.dt;
-  const int most = a.epi == kW8SiluQuant ? 128 : 256;
-  p.BT = a.groups ? a.bt : a.xrows >= most ? most : (a.xrows + 15) / 16 * 16;
+  const int sms = num_sms();
+  p.BT = a.groups ? a.bt : dense_bt(a.xrows, a.N, p.KB, sms);
   const long long wtotal = (long long)p.wrows * (a.groups ? a.groups : 1);
   p.wtotal = (int)wtotal;
-  const int cg = p.BT >= AWQ_W8_PAIR_BT ? 2 : 1;
+  const int cg = p.BT >= kPairLeast ? 2 : 1;
   p.n_tiles = (a.N + kTileW * cg - 1) / (kTileW * cg);
   p.t_tiles = (a.xrows + p.BT - 1) / p.BT;
   // upper bound of the tiles: grouped, each group that has rows adds at most one partly filled token tile
   const long long tt = a.groups ? (a.xrows / p.BT + (a.xrows < a.groups ? a.xrows : a.groups)) : p.t_tiles;
   const long long bound = tt * p.n_tiles;
   if (bound > 0x7FFFFFFF || wtotal > 0x7FFFFFFF) return AWQ_ERR_UNSUPPORTED;
-  const int sms = num_sms();
   // Few tokens: two CTAs per SM, so that the next kernel's weights are under way while this one ends, and K split over a
   // cluster until the tiles fill both halves.
   const bool half = cg == 1 && p.BT <= kHalfMost;
@@ -781,7 +886,7 @@ awq_status w8a8_launch(const W8Args& a) {
   if (half)
     while (p.splits < 8 && bound * p.splits * 2 <= slots && p.KB >= p.splits * 4) p.splits *= 2;
   const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
-  const int part = p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
+  const int part = cg == 2 ? kEpiGroups * 16 * kTileW * 4 : p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
   const int rest = 1024 + kSf * slot + part + 512 + 64 + kEpiGroups * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
   p.ST = ((half ? kW8HalfSmem : kW8Smem) - rest) / stage;
   if (p.ST > 12) p.ST = 12;
