@@ -414,3 +414,19 @@ def test_linear_either_side_of_the_fused_quantizer(M, K):
     y = W.w8a8_linear(x.cuda(), w)
     check_linear(y, R.grid(np64(x)), wv, torch.float16)
     assert torch.equal(y, W.w8a8_linear(W.fp8_quantize(x.cuda()), w, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("E,groups", [(4, 2), (6, 3), (30, 15), (32, 32), (96, 6), (1024, 16)])
+def test_route_close_groups(E, groups):
+    """Group sums that 32 bits cannot order, in groups of one expert, of two and of many; some experts masked."""
+    rng = np.random.default_rng(E * groups)
+    M, tg = 60, max(1, groups // 2)
+    l = (0.5 + rng.integers(0, 3, (M, E)) * 2.0 ** -23).astype(np.float32)
+    l[rng.random((M, E)) < 0.1] = -np.inf
+    bias = (rng.integers(-1, 2, E) * 2.0 ** -26).astype(np.float32)
+    topk = min(5, tg * (E // groups))
+    for b in (None, bias):
+        for score in ("sigmoid", "softmax"):
+            kw = dict(topk=topk, score=score, groups=groups, topk_groups=tg)
+            r = W.moe_route(torch.from_numpy(l).cuda(), bias=None if b is None else torch.from_numpy(b).cuda(), **kw)
+            check_route(r, l, bias=b, **kw)

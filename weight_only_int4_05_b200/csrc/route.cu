@@ -153,12 +153,13 @@ __device__ __forceinline__ void route_top2(float& a, float& b, float oa, float o
 // One warp per token; lane l holds experts l, l + 32, ... (NE of them).
 template <int DT, int NE>
 __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 8 ? 8 : 4) route_kernel(const RouteParams p) {
-  extern __shared__ double route_q[];  // [warps][E]: the choices, for the group sums and the 64-bit path
+  extern __shared__ double route_q[];  // [warps][E + 32]: the choices, for the group sums and the 64-bit path
   pdl_launch_dependents();
   pdl_wait_prior_grids();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool softmax = p.score == AWQ_SCORE_SOFTMAX;
-  float* qs = reinterpret_cast<float*>(route_q + (size_t)warp * p.E);
+  double* own = route_q + (size_t)warp * (p.E + 32);
+  float* qs = reinterpret_cast<float*>(own);
   float bias[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) bias[i] = 0.f;
@@ -201,17 +202,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 8 ? 8 : 4) route_kerne
     }
     bool doubt = false;
     if (p.groups > 1) {
+      // Group g's choices stand at g * pitch: the pitch moves each group by its lanes' banks, so that no two lanes meet.
+      const int pitch = per + share;
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (i * 32 + lane < p.E) qs[i * 32 + lane] = q[i];
+      for (int i = 0; i < NE; ++i) {
+        const int e = i * 32 + lane;
+        const int of = (int)(((float)e + 0.5f) * per_inv);  // e / per: below 1024 the half keeps the product off whole numbers
+        if (e < p.E) qs[e + of * share] = q[i];
+      }
       __syncwarp();
       const int g = lane >> (__ffs(share) - 1);
+      const bool group = g < p.groups;
       float a = -INFINITY, b = -INFINITY;
-      if (g < p.groups) {
-        const float* end = qs + (g + 1) * per;
+      if (group) {
+        const float* end = qs + g * pitch + per;
 #pragma unroll 8
-        for (const float* x = qs + g * per + (lane & (share - 1)); x < end; x += share) route_top2(a, b, *x, -INFINITY);
+        for (const float* x = qs + g * pitch + (lane & (share - 1)); x < end; x += share) route_top2(a, b, *x, -INFINITY);
       }
       for (int d = 1; d < share; d <<= 1)
         route_top2(a, b, __shfl_xor_sync(0xFFFFFFFFu, a, d), __shfl_xor_sync(0xFFFFFFFFu, b, d));
@@ -224,15 +231,52 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 8 ? 8 : 4) route_kerne
         before += (w > v || (w == v && o < g)) ? 1 : 0;
         near |= o != g && !(fabsf(w - v) > (softmax ? 0x1p-17f : 0x1p-20f) * size);
       }
-      const bool in = before < p.topk_groups;
       // A doubtful neighbour matters where the border runs between the two: the last group in or the first one out.
-      doubt = g < p.groups && near && p.topk_groups < p.groups &&
+      doubt = group && near && p.topk_groups < p.groups &&
               (before == p.topk_groups - 1 || before == p.topk_groups || !(size < 1e30f));
-      const uint32_t kept = __ballot_sync(0xFFFFFFFFu, g < p.groups && in);
+      if (__any_sync(0xFFFFFFFFu, doubt) && !softmax) {
+        // The groups' sums in 64 bits, where each group's two largest are clear of its third (or the whole token again).
+        float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY;
+        int i0 = 0, i1 = 0;
+        if (group) {
+#pragma unroll 8
+          for (int i = 0; i < per; ++i) {
+            const float x = qs[g * pitch + i];
+            t2 = fmaxf(t2, fminf(x, t1));
+            if (x > t0) {
+              t1 = t0;
+              i1 = i0;
+              t0 = x;
+              i0 = i;
+            } else if (x > t1) {
+              t1 = x;
+              i1 = i;
+            }
+          }
+        }
+        double sum = -INFINITY;
+        doubt = false;
+        if (group) {
+          auto choice = [&](int i) {
+            const int e = g * per + i;
+            const float l0 = route_clean(route_logit<DT>(p.logits, (size_t)m * p.E + e)), b0 = p.bias ? p.bias[e] : 0.f;
+            return l0 == -INFINITY || !(b0 >= kLeastBias) ? kMaskedChoice : route_score(p, l0, 0.f, 1.0) + (double)b0;
+          };
+          sum = choice(i0);
+          if (per > 1) sum += choice(i1);
+          doubt = per > 2 && !(t1 - t2 > 0x1p-20f * 2.f + 0x1p-22f * (fabsf(t1) + fabsf(t2)));
+        }
+        before = 0;
+        for (int o = 0; o < p.groups; ++o) {
+          const double w = __shfl_sync(0xFFFFFFFFu, sum, o * share);
+          before += (w > sum || (w == sum && o < g)) ? 1 : 0;
+        }
+      }
+      const uint32_t kept = __ballot_sync(0xFFFFFFFFu, group && before < p.topk_groups);
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         const int e = i * 32 + lane;
-        const int of = (int)(((float)e + 0.5f) * per_inv);  // e / per: below 1024 the half keeps the product off whole numbers
+        const int of = (int)(((float)e + 0.5f) * per_inv);
         if (e < p.E && !((kept >> (of * share)) & 1u)) q[i] = -INFINITY;
       }
     }
@@ -307,7 +351,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 8 ? 8 : 4) route_kerne
     }
     if (again) {
       __syncwarp();
-      route_exact<DT>(p, m, route_q + (size_t)warp * p.E);
+      route_exact<DT>(p, m, own);
       continue;
     }
     // The scores of the taken in 64 bits.
@@ -372,7 +416,7 @@ awq_status moe_route_launch(const void* logits, int dt, const float* bias, int M
   long long grid = ((long long)M + kRouteWarps - 1) / kRouteWarps;
   const long long cap = (long long)num_sms() * 16;
   if (grid > cap) grid = cap;
-  const size_t smem = (size_t)kRouteWarps * E * sizeof(double);  // at most 32 KB
+  const size_t smem = (size_t)kRouteWarps * (E + 32) * sizeof(double);  // at most 33 KB
   const cudaError_t e = dt == AWQ_DTYPE_F32   ? route_pick<AWQ_DTYPE_F32>(p, (unsigned)grid, smem, st)
                         : dt == AWQ_DTYPE_F16 ? route_pick<AWQ_DTYPE_F16>(p, (unsigned)grid, smem, st)
                                               : route_pick<AWQ_DTYPE_BF16>(p, (unsigned)grid, smem, st);
