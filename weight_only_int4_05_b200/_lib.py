@@ -40,6 +40,8 @@ def lib_path() -> str:
 
 def load() -> ctypes.CDLL:
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -152,7 +152,7 @@ __device__ __forceinline__ void route_top2(float& a, float& b, float oa, float o
 
 // One warp per token; lane l holds experts l, l + 32, ... (NE of them).
 template <int DT, int NE>
-__global__ void __launch_bounds__(32 * kRouteWarps, NE <= 8 ? 8 : 4) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : NE <= 16 ? 4 : 2) route_kernel(const RouteParams p) {
   extern __shared__ double route_q[];  // [warps][E + 32]: the choices, for the group sums and the 64-bit path
   pdl_launch_dependents();
   pdl_wait_prior_grids();

@@ -36,10 +36,12 @@ namespace {
 
 constexpr int kTileW = 128;        // weight rows per accumulator and CTA
 constexpr int kBlkBytes = 128;     // bytes of K per k-block: one swizzle row, one scale block
-constexpr int kEpiGroups = 2;      // epilogue warpgroups
+template <int CG>
+constexpr int kEpi = 2;  // epilogue warpgroups
 constexpr int kXqMost = 16;        // tokens up to which the epilogue warps quantize x: 8 warps of 2 rows
 constexpr int kHalfMost = 32;      // tokens per tile up to which a CTA takes half an SM's shared memory
-constexpr int kW8Threads = 128 + 128 * kEpiGroups;
+template <int CG>
+constexpr int kW8Threads = 128 + 128 * kEpi<CG>;
 constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on sm_100
 constexpr int kW8HalfSmem = 115712;  // two blocks per SM (1 KB of each block's share is the system's)
 constexpr int kPairLeast = 64;     // tokens per tile from which two CTAs work on it together
@@ -358,15 +360,15 @@ __device__ __forceinline__ void w8_quantize_x(const W8Params& p, const W8Tile& t
 }  // namespace
 
 template <int EPI, int CG, bool XQ>
-__global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const __grid_constant__ W8Maps maps, const W8Params p) {
+__global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(const __grid_constant__ W8Maps maps, const W8Params p) {
   constexpr int NA = kAtomsA<EPI>;
   extern __shared__ uint8_t w8_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w8_smem_raw) + 1023) & ~uintptr_t(1023));
   const int stage = w8_stage(NA, p.BT / CG), slot = w8_sf_slot(NA, p.BT);
   uint8_t* sf = smem + p.ST * stage;
   float* part = reinterpret_cast<float*>(sf + kSf * slot);  // splits > 1: [NA * BT][128] partial sums
-  // a pair: [kEpiGroups][16][128], the epilogue's turning space in its place
-  uint64_t* full = reinterpret_cast<uint64_t*>(part + (CG == 2 ? kEpiGroups * 16 * kTileW : p.splits > 1 ? NA * p.BT * kTileW : 0));
+  // a pair: [kEpi][16][128], the epilogue's turning space in its place
+  uint64_t* full = reinterpret_cast<uint64_t*>(part + (CG == 2 ? kEpi<CG> * 16 * kTileW : p.splits > 1 ? NA * p.BT * kTileW : 0));
   uint64_t* empty = full + p.ST;
   uint64_t* sf_full = empty + p.ST;
   uint64_t* sf_empty = sf_full + kSf;
@@ -378,28 +380,28 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_free + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 2);  // [2] the epilogue warps' common decision
-  uint32_t* amax = tmem_slot + 4;  // [kEpiGroups][2][4][16] token maxima of the quantizing epilogue
-  int* tabs = reinterpret_cast<int*>(amax + kEpiGroups * 128);    // grouped: tile_start and row_start
+  uint32_t* amax = tmem_slot + 4;  // one CTA: [kEpi][2][4][16] token maxima of the quantizing epilogue
+  int* tabs = reinterpret_cast<int*>(amax + kEpi<1> * 128);    // grouped: tile_start and row_start
 
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = (CG == 2 || p.splits > 1) ? (int)cluster_rank() : 0;
   const int csize = CG == 2 ? 2 : p.splits;  // CTAs that share a tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ST; ++s) {
-      mbar_init(&full[s], XQ ? 1 + 4 * kEpiGroups : 1);
+      mbar_init(&full[s], XQ ? 1 + 4 * kEpi<CG> : 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kSf; ++s) {
-      mbar_init(&sf_full[s], XQ ? 1 + 4 * kEpiGroups : CG);
+      mbar_init(&sf_full[s], XQ ? 1 + 4 * kEpi<CG> : CG);
       mbar_init(&sf_empty[s], 1);
     }
     mbar_init(&acc_full[0], 1);
     mbar_init(&acc_full[1], 1);
-    mbar_init(&acc_free[0], 4 * kEpiGroups * CG);
-    mbar_init(&acc_free[1], 4 * kEpiGroups * CG);
+    mbar_init(&acc_free[0], 4 * kEpi<CG> * CG);
+    mbar_init(&acc_free[1], 4 * kEpi<CG> * CG);
     mbar_init(drain, 1);
-    mbar_init(part_full, 4 * kEpiGroups * p.splits);
-    mbar_init(part_free, 4 * kEpiGroups * p.splits);
+    mbar_init(part_full, 4 * kEpi<CG> * p.splits);
+    mbar_init(part_free, 4 * kEpi<CG> * p.splits);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.w);
@@ -624,9 +626,9 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
     XqState xq;
     // All epilogue warps take the same way out: one thread reads the flag for all.
     auto all_ok = [&]() {
-      named_barrier_sync(1, 128 * kEpiGroups);
+      named_barrier_sync(1, 128 * kEpi<CG>);
       if (threadIdx.x == 128) stop[decisions & 1] = *abort_flag;
-      named_barrier_sync(1, 128 * kEpiGroups);
+      named_barrier_sync(1, 128 * kEpi<CG>);
       return stop[decisions++ & 1] == 0;
     };
     auto release = [&]() {
@@ -659,13 +661,13 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
           release();
           held = false;
         }
-        for (int i = wg; i < chunks; i += kEpiGroups) {
+        for (int i = wg; i < chunks; i += kEpi<CG>) {
           const int c = CW * (buf ? i : chunks - 1 - i);  // the shared columns are the first buffer's last, the second's first
           uint32_t v[CW], u[CW];
           tmem_ld_cols<CW>(acc + (uint32_t)c, v);
           if (NA == 2) tmem_ld_cols<CW>(acc + (uint32_t)(p.BT + c), u);
           tmem_wait_ld();
-          if (held && (apart ? i + kEpiGroups >= chunks : i + kEpiGroups >= shared)) {
+          if (held && (apart ? i + kEpi<CG> >= chunks : i + kEpi<CG> >= shared)) {
             release();
             held = false;
           }
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
       }
       // ---- split K: the parts of all CTAs of the cluster are summed in rank order, each CTA doing its share of the tokens
       if (done > 0) warp_wait(part_free, (unsigned)((done - 1) & 1), p.status, abort_flag);
-      for (int c = 16 * wg; c < NA * p.BT; c += 16 * kEpiGroups) {
+      for (int c = 16 * wg; c < NA * p.BT; c += 16 * kEpi<CG>) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
         tmem_wait_ld();
@@ -702,7 +704,7 @@ __global__ void __launch_bounds__(kW8Threads, CG == 1 ? 2 : 1) w8a8_kernel(const
       if (!all_ok()) break;
       const int share = p.BT / p.splits;  // tokens per CTA, a multiple of 2
 #pragma unroll 2
-      for (int c = rank * share + 2 * wg; c < min((rank + 1) * share, t.rows); c += 2 * kEpiGroups) {
+      for (int c = rank * share + 2 * wg; c < min((rank + 1) * share, t.rows); c += 2 * kEpi<CG>) {
         float v[8][2], u[8][2];  // all parts in flight at once
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
@@ -784,7 +786,7 @@ cudaError_t launch_one(const W8Maps& maps, const W8Params& p, int grid, int smem
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kW8Threads);
+  cfg.blockDim = dim3(kW8Threads<CG>);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -886,8 +888,8 @@ awq_status w8a8_launch(const W8Args& a) {
   if (half)
     while (p.splits < 8 && bound * p.splits * 2 <= slots && p.KB >= p.splits * 4) p.splits *= 2;
   const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
-  const int part = cg == 2 ? kEpiGroups * 16 * kTileW * 4 : p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
-  const int rest = 1024 + kSf * slot + part + 512 + 64 + kEpiGroups * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
+  const int part = cg == 2 ? kEpi<2> * 16 * kTileW * 4 : p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
+  const int rest = 1024 + kSf * slot + part + 512 + 64 + kEpi<1> * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
   p.ST = ((half ? kW8HalfSmem : kW8Smem) - rest) / stage;
   if (p.ST > 12) p.ST = 12;
   if (p.ST < 2) return AWQ_ERR_UNSUPPORTED;
