@@ -253,36 +253,49 @@ __global__ void __launch_bounds__(256) scatter_kernel(const uint16_t* x, const i
   }
 }
 
-// y_m = round(sum_j w_mj d[pos_mj]), slots in order, 32 bits until the end.  One thread per 4 columns of a token.
-__global__ void __launch_bounds__(256) combine_kernel(const float* d, const int* pos,
-                                                      const float* weights, int M, int topk, int N, int dt,
-                                                      uint16_t* y) {
+// y_m = round(sum_j w_mj d[pos_mj]), slots in order, 32 bits until the end.  One thread per 4 columns of a token; the rows
+// of 4 slots are fetched together, since a fetch after each slot's place would wait for memory twice per slot.
+template <bool WIDE>
+__global__ void __launch_bounds__(256) combine_kernel(const float* d, const int* pos, const float* weights, int M, int topk,
+                                                      int N, int dt, uint16_t* y) {
   pdl_launch_dependents();
   pdl_wait_prior_grids();
   const int cols = (N + 3) / 4;
   const long long items = (long long)M * cols;
-  const bool wide = (N & 3) == 0;
   for (long long it = (long long)blockIdx.x * blockDim.x + threadIdx.x; it < items;
        it += (long long)gridDim.x * blockDim.x) {
-    const long long m = it / cols;
-    const int n = (int)(it - m * cols) * 4;
+    const int m = (int)(it / cols);
+    const int n = (int)(it - (long long)m * cols) * 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < topk; ++j) {
-      const int r = pos[m * topk + j];
-      if (r < 0) continue;
-      const float w = weights[m * topk + j];
-      const float* src = d + (size_t)r * N + n;
-      float4 v;
-      if (wide) v = *reinterpret_cast<const float4*>(src);
-      else v = make_float4(src[0], n + 1 < N ? src[1] : 0.f, n + 2 < N ? src[2] : 0.f, n + 3 < N ? src[3] : 0.f);
-      s.x = fmaf(w, v.x, s.x);
-      s.y = fmaf(w, v.y, s.y);
-      s.z = fmaf(w, v.z, s.z);
-      s.w = fmaf(w, v.w, s.w);
+    for (int j0 = 0; j0 < topk; j0 += 4) {
+      int r[4];
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[j] = j0 + j < topk ? pos[(size_t)m * topk + j0 + j] : -1;
+        w[j] = j0 + j < topk ? weights[(size_t)m * topk + j0 + j] : 0.f;
+      }
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r[j] < 0) continue;
+        const float* src = d + (size_t)r[j] * N + n;
+        if (WIDE) v[j] = *reinterpret_cast<const float4*>(src);
+        else v[j] = make_float4(src[0], n + 1 < N ? src[1] : 0.f, n + 2 < N ? src[2] : 0.f, n + 3 < N ? src[3] : 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (r[j] < 0) continue;  // a weight of an empty slot may be anything
+        s.x = fmaf(w[j], v[j].x, s.x);
+        s.y = fmaf(w[j], v[j].y, s.y);
+        s.z = fmaf(w[j], v[j].z, s.z);
+        s.w = fmaf(w[j], v[j].w, s.w);
+      }
     }
-    uint16_t* o = y + m * N + n;
+    uint16_t* o = y + (size_t)m * N + n;
     const float f[4] = {s.x, s.y, s.z, s.w};
-    if (wide) {
+    if (WIDE) {
       uint2 v;
       v.x = f32_to_16(f[0], dt) | ((uint32_t)f32_to_16(f[1], dt) << 16);
       v.y = f32_to_16(f[2], dt) | ((uint32_t)f32_to_16(f[3], dt) << 16);
@@ -364,7 +377,8 @@ awq_status moe_launch(const MoeArgs& a) {
   st = w8a8_launch(down);
   if (st != AWQ_OK) return st;
   blocks = ((long long)a.M * ((a.N + 3) / 4) + 255) / 256;
-  e = launch_pdl(combine_kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, a.st,
+  auto combine = a.N % 4 == 0 ? combine_kernel<true> : combine_kernel<false>;
+  e = launch_pdl(combine, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, a.st,
                  reinterpret_cast<const float*>(ws + l.d), static_cast<const int*>(t.pos), a.weights, a.M, a.topk, a.N,
                  a.dt, a.y);
   return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA;

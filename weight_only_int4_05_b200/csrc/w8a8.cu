@@ -39,6 +39,7 @@ constexpr int kBlkBytes = 128;     // bytes of K per k-block: one swizzle row, o
 template <int CG>
 constexpr int kEpi = 2;  // epilogue warpgroups
 constexpr int kXqMost = 16;        // tokens up to which the epilogue warps quantize x: 8 warps of 2 rows
+constexpr int kPartLeast = 8;      // k-blocks per part of a split K: joining parts takes about as long as 8 of them
 constexpr int kHalfMost = 32;      // tokens per tile up to which a CTA takes half an SM's shared memory
 template <int CG>
 constexpr int kW8Threads = 128 + 128 * kEpi<CG>;
@@ -886,7 +887,7 @@ awq_status w8a8_launch(const W8Args& a) {
   const int slots = half ? 2 * sms : sms;
   p.splits = 1;
   if (half)
-    while (p.splits < 8 && bound * p.splits * 2 <= slots && p.KB >= p.splits * 4) p.splits *= 2;
+    while (p.splits < 8 && bound * p.splits * 2 <= slots && p.KB >= p.splits * 2 * kPartLeast) p.splits *= 2;
   const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
   const int part = cg == 2 ? kEpi<2> * 16 * kTileW * 4 : p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
   const int rest = 1024 + kSf * slot + part + 512 + 64 + kEpi<1> * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
