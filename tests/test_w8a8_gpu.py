@@ -430,3 +430,21 @@ def test_route_close_groups(E, groups):
             kw = dict(topk=topk, score=score, groups=groups, topk_groups=tg)
             r = W.moe_route(torch.from_numpy(l).cuda(), bias=None if b is None else torch.from_numpy(b).cuda(), **kw)
             check_route(r, l, bias=b, **kw)
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 130, 6016), (64, 100, 8192), (90, 38, 4112), (300, 260, 5120), (700, 60, 3088)])
+def test_linear_few_outputs_long_k(M, N, K):
+    """Tiles too few to fill the GPU and a long K: it is split over a cluster, whose parts meet in shared memory."""
+    rng = np.random.default_rng(M + N)
+    w, wv = matrix(rng, (N, K))
+    x = activations(rng, M, K, torch.bfloat16)
+    y = W.w8a8_linear(x.cuda(), w)
+    check_linear(y, R.grid(np64(x)), wv, torch.bfloat16)
+    assert torch.equal(y, W.w8a8_linear(x.cuda(), w))
+    status_ok()
+
+
+@pytest.mark.parametrize("M,E,topk,K,I,N", [(60, 2, 2, 4096, 64, 100), (120, 2, 1, 2048, 2048, 64), (200, 3, 1, 64, 4096, 40)])
+def test_moe_few_tiles_long_k(M, E, topk, K, I, N):
+    rng = np.random.default_rng(M + K)
+    check_moe(M, E, topk, K, I, N, torch.float16, choose(rng, M, E, topk), rng)

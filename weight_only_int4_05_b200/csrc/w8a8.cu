@@ -45,6 +45,7 @@ template <int CG>
 constexpr int kW8Threads = 128 + 128 * kEpi<CG>;
 constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on sm_100
 constexpr int kW8HalfSmem = 115712;  // two blocks per SM (1 KB of each block's share is the system's)
+constexpr int kSplitMost = 64;     // tokens per tile up to which K is split
 constexpr int kPairLeast = 64;     // tokens per tile from which two CTAs work on it together
 constexpr int kSf = 4;             // scale slots (4 k-blocks each) in shared memory
 constexpr int kSfTmem = 2;         // and in tensor memory
@@ -804,22 +805,39 @@ cudaError_t launch_one(const W8Maps& maps, const W8Params& p, int grid, int smem
 
 }  // namespace
 
-// The token tile of the dense product.  Up to 32 tokens one tile; above, the tile whose waves over the SMs take the least
-// time by a count of cycles: per k-block the larger of the products (2 per token), of their issue (300) and of the operands'
-// way from L2 (64 bytes a cycle and SM), then the last tile's epilogue (30 per token) and a tile's start.
-int dense_bt(int M, int N, int KB, int sms) {
-  if (M <= kHalfMost) return (M + 15) / 16 * 16;
-  int best = 16;
+struct W8Shape {
+  int bt, cg, splits;  // tokens per tile, CTAs per tile (1 or 2), parts of K
+};
+
+// Parts of K for one-CTA tiles that fill less than half of `slots`, each of kPartLeast k-blocks or more.
+int split_k(long long tiles, int KB, int slots) {
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= slots && KB >= splits * 2 * kPartLeast) splits *= 2;
+  return splits;
+}
+
+// The dense product's tile.  Up to 32 tokens one token tile; above, the tile whose waves over the SMs take the least time by
+// a count of cycles: per k-block the larger of the products (2 per token), of their issue (300) and of the operands' way from
+// L2 (64 bytes a cycle and SM), a tile's start (1000), the joining of a split K (3000), and the last tile's epilogue (30 per token).
+W8Shape dense_shape(int M, int N, int KB, int sms) {
+  if (M <= kHalfMost) {
+    const int bt = (M + 15) / 16 * 16;
+    return W8Shape{bt, 1, split_k((N + kTileW - 1) / kTileW, KB, 2 * sms)};
+  }
+  W8Shape best{256, 2, 1};
   double least = 1e30;
   for (int bt = 48; bt <= 256; bt += 16) {
-    const int cg = bt >= kPairLeast ? 2 : 1;
-    const double tiles = (double)((M + bt - 1) / bt) * ((N + kTileW * cg - 1) / (kTileW * cg));
-    const double waves = ceil(tiles / (sms / cg));
-    const double block = fmax(fmax(2.0 * bt, 300.0), (kTileW + (double)bt / cg) * kBlkBytes / 64.0);
-    const double cost = waves * (KB * block + 1000.0) + 30.0 * bt;
-    if (cost < least) {
-      least = cost;
-      best = bt;
+    for (int cg = bt < kPairLeast ? 1 : 2; cg >= (bt <= kSplitMost ? 1 : 2); --cg) {
+      const long long tiles = (long long)((M + bt - 1) / bt) * ((N + kTileW * cg - 1) / (kTileW * cg));
+      const int splits = cg == 1 ? split_k(tiles, KB, sms) : 1;
+      const double waves = ceil((double)tiles / (sms / (cg * splits)));
+      const double block = fmax(fmax(2.0 * bt, 300.0), (kTileW + (double)bt / cg) * kBlkBytes / 64.0);
+      const double cost =
+          waves * (ceil((double)KB / splits) * block + 1000.0) + 30.0 * bt + (splits > 1 ? 3000.0 : 0.0);
+      if (cost < least) {
+        least = cost;
+        best = W8Shape{bt, cg, splits};
+      }
     }
     if (bt >= M) break;
   }
@@ -871,23 +889,33 @@ awq_status w8a8_launch(const W8Args& a) {
   p.groups = a.groups;
   p.dt = a.dt;
   const int sms = num_sms();
-  p.BT = a.groups ? a.bt : dense_bt(a.xrows, a.N, p.KB, sms);
   const long long wtotal = (long long)p.wrows * (a.groups ? a.groups : 1);
+  // upper bound of the token tiles: grouped, each group that has rows adds at most one partly filled tile
+  auto token_tiles = [&](int bt) {
+    return a.groups ? (long long)a.xrows / bt + (a.xrows < a.groups ? a.xrows : a.groups) : ((long long)a.xrows + bt - 1) / bt;
+  };
+  W8Shape shape;
+  if (a.groups) {
+    shape = W8Shape{a.bt, a.bt >= kPairLeast ? 2 : 1, 1};
+    const long long single = token_tiles(a.bt) * ((a.N + kTileW - 1) / kTileW);
+    if (a.bt <= kSplitMost) {  // few tiles of a long K are split instead of paired
+      const int splits = split_k(single, p.KB, a.bt <= kHalfMost ? 2 * sms : sms);
+      if (shape.cg == 1 || splits > 1) shape = W8Shape{a.bt, 1, splits};
+    }
+  } else {
+    shape = dense_shape(a.xrows, a.N, p.KB, sms);
+  }
+  const int cg = shape.cg;
+  p.BT = shape.bt;
+  p.splits = shape.splits;
   p.wtotal = (int)wtotal;
-  const int cg = p.BT >= kPairLeast ? 2 : 1;
   p.n_tiles = (a.N + kTileW * cg - 1) / (kTileW * cg);
-  p.t_tiles = (a.xrows + p.BT - 1) / p.BT;
-  // upper bound of the tiles: grouped, each group that has rows adds at most one partly filled token tile
-  const long long tt = a.groups ? (a.xrows / p.BT + (a.xrows < a.groups ? a.xrows : a.groups)) : p.t_tiles;
-  const long long bound = tt * p.n_tiles;
+  p.t_tiles = (int)token_tiles(p.BT);
+  const long long bound = token_tiles(p.BT) * p.n_tiles;
   if (bound > 0x7FFFFFFF || wtotal > 0x7FFFFFFF) return AWQ_ERR_UNSUPPORTED;
-  // Few tokens: two CTAs per SM, so that the next kernel's weights are under way while this one ends, and K split over a
-  // cluster until the tiles fill both halves.
+  // Few tokens: two CTAs per SM, so that the next kernel's weights are under way while this one ends.
   const bool half = cg == 1 && p.BT <= kHalfMost;
   const int slots = half ? 2 * sms : sms;
-  p.splits = 1;
-  if (half)
-    while (p.splits < 8 && bound * p.splits * 2 <= slots && p.KB >= p.splits * 2 * kPartLeast) p.splits *= 2;
   const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
   const int part = cg == 2 ? kEpi<2> * 16 * kTileW * 4 : p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
   const int rest = 1024 + kSf * slot + part + 512 + 64 + kEpi<1> * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
