@@ -404,12 +404,12 @@ def test_moe_many_experts(E, M):
     check_moe(M, E, 2, 32, 16, 24, torch.bfloat16, torch.from_numpy(rng.integers(0, E, (M, 2))).int(), rng)
 
 
-@pytest.mark.parametrize("M", [3, 15, 16, 17, 32, 33, 48])
-@pytest.mark.parametrize("K", [400, 1536])
-def test_linear_either_side_of_the_fused_quantizer(M, K):
+@pytest.mark.parametrize("M", [3, 15, 16, 17, 32, 33, 47, 64, 65, 200])
+@pytest.mark.parametrize("N,K", [(520, 400), (520, 1536), (96, 6160), (4104, 2048)])
+def test_linear_either_side_of_the_fused_quantizer(M, N, K):
     """Up to 16 tokens the product quantizes x itself: the same bits as from the quantizer's arrays."""
     rng = np.random.default_rng(M + K)
-    w, wv = matrix(rng, (520, K))
+    w, wv = matrix(rng, (N, K))
     x = activations(rng, M, K, torch.float16)
     y = W.w8a8_linear(x.cuda(), w)
     check_linear(y, R.grid(np64(x)), wv, torch.float16)
