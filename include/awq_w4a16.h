@@ -452,7 +452,8 @@ awq_status moe_route(const void* d_logits, int dtype, const float* d_bias, int M
  *   Q the 8-bit quantizer of fp8_quantize (applied to the fp32 values silu(a) b), sums in fp32, the slots j in order.
  *   d_x [M][K] of dtype;  d_ids [M][topk] int32, d_weights [M][topk] fp32;  gate|up: 8-bit matrices [E][2 I][K], the gate
  *   rows of an expert before its up rows;  down: [E][N][I];  d_y [M][N] of dtype, written.  An id outside 0 .. E - 1 adds nothing
- *   (a padded token, an expert that lives elsewhere); an expert may occur twice in a row.  topk <= 32, M * topk <= 2^24.
+ *   (a padded token, an expert that lives elsewhere); an expert may occur twice in a row.  topk <= 32, M * topk <= 2^24,
+ *   E <= 1024, E * 2 I and E * N <= 2^30.
  *   d_workspace: w8a8_moe_workspace_bytes(...) bytes; calls in flight must not share it.
  * Errors: as w8a8_linear.
  */

@@ -27,7 +27,8 @@ def test_sizes(L):
     assert L.w8a8_moe_workspace_bytes(4, 8, 2, 512, 256, 512) >= 8 * (512 + 256 + 4 * 512)
     for bad in ((0, 8, 2, 512, 256, 512), (4, 0, 2, 512, 256, 512), (4, 1025, 2, 512, 256, 512),
                 (4, 8, 0, 512, 256, 512), (4, 8, 33, 512, 256, 512), (4, 8, 2, 500, 256, 512),
-                (4, 8, 2, 512, 250, 512), (4, 8, 2, 512, 256, 0), (1 << 22, 8, 8, 512, 256, 512)):
+                (4, 8, 2, 512, 250, 512), (4, 8, 2, 512, 256, 0), (1 << 22, 8, 8, 512, 256, 512),
+                (4, 1024, 2, 512, (1 << 19) + 16, 512), (4, 1024, 2, 512, 256, (1 << 20) + 1)):
         assert L.w8a8_moe_workspace_bytes(*bad) == Z, bad
 
 

@@ -446,7 +446,7 @@ awq_status moe_route(const void* d_logits, int dtype, const float* d_bias, int M
 static bool moe_sizes_ok(int M, int E, int topk, int K, int I, int N) {
   return size_ok(M, 1 << 24, 1) && size_ok(E, 1024, 1) && topk >= 1 && topk <= 32 && (long long)M * topk <= (1 << 24) &&
          size_ok(K, kMaxK, 16) && size_ok(I, kMaxK, 16) && size_ok(N, kMaxN, 1) &&
-         (long long)E * 2 * I <= 0x7FFFFFFF && (long long)E * N <= 0x7FFFFFFF;
+         (long long)E * 2 * I <= (1 << 30) && (long long)E * N <= (1 << 30);
 }
 
 size_t w8a8_moe_workspace_bytes(int M, int E, int topk, int K, int I, int N) {

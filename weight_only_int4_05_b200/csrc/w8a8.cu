@@ -502,6 +502,8 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
     }
     __syncwarp();
   } else if (warp == 1) {
+    // Nothing to multiply before x is there; without this the waits below would count the kernel before this one's time.
+    pdl_wait_prior_grids();
     if (CG == 1 || rank == 0) {
       int s = 0, cs = 0, ct = 0, done = 0;  // ring stage, scale slots in shared and tensor memory, tiles
       unsigned phase = 0, cphase = 0;
@@ -917,10 +919,14 @@ awq_status w8a8_launch(const W8Args& a) {
   const bool half = cg == 1 && p.BT <= kHalfMost;
   const int slots = half ? 2 * sms : sms;
   const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
-  const int part = cg == 2 ? kEpi<2> * 16 * kTileW * 4 : p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
-  const int rest = 1024 + kSf * slot + part + 512 + 64 + kEpi<1> * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
-  p.ST = ((half ? kW8HalfSmem : kW8Smem) - rest) / stage;
-  if (p.ST > 12) p.ST = 12;
+  int rest;
+  for (;; p.splits /= 2) {  // the parts of a split K and the tables of many groups may leave too little for the ring
+    const int part = cg == 2 ? kEpi<2> * 16 * kTileW * 4 : p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
+    rest = 1024 + kSf * slot + part + 512 + 64 + kEpi<1> * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
+    p.ST = ((half ? kW8HalfSmem : kW8Smem) - rest) / stage;
+    if (p.ST > 12) p.ST = 12;
+    if (p.ST >= 2 || p.splits == 1) break;
+  }
   if (p.ST < 2) return AWQ_ERR_UNSUPPORTED;
   const int sfc = kSfTmem * w8_sf_cols(atoms, p.BT), acc = atoms * p.BT;
   p.acc_off = acc < 512 - sfc - acc ? acc : 512 - sfc - acc;
