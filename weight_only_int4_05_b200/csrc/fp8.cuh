@@ -89,12 +89,17 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 // A whole warp waits for the phase with the given parity; all lanes get the same answer.  False after kWaitLimitNs
-// (recorded in *status) or once another role of the CTA gave up; either way *abort_flag is set.
+// (recorded in *status) or once another role of the CTA gave up; either way *abort_flag is set.  CLUSTER: acquire what other
+// CTAs of the cluster wrote before they arrived, for this warp's own loads (several hundred cycles more per wait).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned* status, volatile int* abort_flag) {
-  if (__all_sync(0xFFFFFFFFu, mbar_try_wait_cluster(bar, parity))) return true;
+  auto passed = [&]() {
+    return __all_sync(0xFFFFFFFFu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity));
+  };
+  if (passed()) return true;
   const unsigned long long t0 = globaltimer_ns();
   for (unsigned it = 0;; ++it) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait_cluster(bar, parity))) return true;
+    if (passed()) return true;
     if ((it & 63u) == 63u) {
       const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
       if (__any_sync(0xFFFFFFFFu, late || *abort_flag)) {

@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
       release();
       // one lane per CTA of the cluster: each arrival carries a release, and eight in a row would take microseconds
       if (lane < p.splits) mbar_arrive_cluster(cluster_addr(part_full, (uint32_t)lane));
-      warp_wait(part_full, (unsigned)(done & 1), p.status, abort_flag);
+      warp_wait<true>(part_full, (unsigned)(done & 1), p.status, abort_flag);
       if (!all_ok()) break;
       const int share = p.BT / p.splits;  // tokens per CTA, a multiple of 2
 #pragma unroll 2
