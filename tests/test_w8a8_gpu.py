@@ -153,9 +153,17 @@ def test_linear_writes_its_output_alone():
 def check_route(r, logits, **kw):
     ids, w = R.route(logits, **kw)
     assert np.array_equal(r.ids.cpu().numpy(), ids)
-    # the weights are 64-bit values rounded once: half a step of fp32, and one more for a value next to a tie; below fp32's
-    # least normal value its steps stop shrinking at 2^-149 (a sigmoid of -200 is 1e-87, which rounds to 0)
-    off = np.abs(np64(r.weights) - w) - (2.0 ** -23 * np.abs(w) + 2.0 ** -149)
+    # 32-bit weights, in units of 2^-24 relative.  Sigmoid: the exponential 4 (2 ulp), 1 + e and the quotient 1 each, so 6;
+    # renormalised by a sum of such terms (6, and 5 additions) with a quotient and the scale's product: 6 + 11 + 2 = 19.
+    # Softmax: l - top rounds by 1/2 unit of |l - top| = |ln p/pmax|, the exponential 4; the sum of up to 1024 terms takes 37
+    # additions and the terms' own errors (4, and sum p |ln p/pmax| / 2 <= 4); two quotients' and the scale's roundings: 64 is
+    # above all of them but |ln p/pmax|.  Below fp32's least normal value its steps stop shrinking at 2^-149; divided by a sum
+    # of at least 2^-20 that is 2^-129.
+    l = np.where(np.isnan(logits), -np.inf, np.minimum(logits.astype(np.float64), np.finfo(np.float32).max))
+    with np.errstate(invalid="ignore"):
+        far = np.abs(np.take_along_axis(l, ids, 1) - l.max(1, keepdims=True)) if kw["score"] == "softmax" else 0.0
+    far = np.where(np.isfinite(far), far, 0.0)
+    off = np.abs(np64(r.weights) - w) - ((64 + far) * 2.0 ** -24 * np.abs(w) + 2.0 ** -126)
     assert off.max() <= 0, off.max()
 
 

@@ -7,7 +7,7 @@
 // works in 32 bits and looks at the gaps that its choice rests on.  Where each is wider than the scores' error (or the two
 // experts have the same logit and bias, a true tie), the 64-bit order is the same; where one is not, the few experts in
 // question are compared in 64 bits; where a border between groups is in doubt, the warp does the token again in 64 bits.
-// The weights of the chosen are 64-bit values rounded once in any case.
+// The weights are 32-bit values of the chosen experts' scores.
 #include "fp8.cuh"
 
 namespace awq {
@@ -282,24 +282,47 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : 
     }
     float mine = -INFINITY;  // lane k: the k-th largest choice; lane topk: the first one left out
     int id = 0, count = 0;
+    // Each lane knows its two largest (the first places among equals); the lane that gives one moves up, and when one has
+    // given both, all look again.
+    float b0, b1;
+    int i0, i1, known;
+    uint32_t gone = 0;  // bit i: this lane's expert i is taken
+    auto look = [&]() {
+      b0 = b1 = -INFINITY;
+      i0 = i1 = 0;
+      known = 2;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const float x = (gone >> i) & 1u ? -INFINITY : q[i];
+        if (x > b0) {
+          b1 = b0;
+          i1 = i0;
+          b0 = x;
+          i0 = i;
+        } else if (x > b1) {
+          b1 = x;
+          i1 = i;
+        }
+      }
+    };
+    look();
     auto take = [&]() {  // the next one, the lowest index among equals; false if none is left or no lane
-      float best = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) best = fmaxf(best, q[i]);
-      const float bq = route_unkey(__reduce_max_sync(0xFFFFFFFFu, route_key(best)));
+      const float bq = route_unkey(__reduce_max_sync(0xFFFFFFFFu, route_key(b0)));
       if (count == 32 || bq == -INFINITY) return false;
-      uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-      for (int i = NE - 1; i >= 0; --i)
-        if (q[i] == bq) at = (uint32_t)(i * 32 + lane);
-      const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, at);
+      const uint32_t own_at = (uint32_t)(i0 * 32 + lane);
+      const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, b0 == bq ? own_at : 0xFFFFFFFFu);
       if (lane == count) {
         mine = bq;
         id = (int)e;
       }
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (e == (uint32_t)(i * 32 + lane)) q[i] = -INFINITY;
+      if (e == own_at) {
+        gone |= 1u << i0;
+        b0 = b1;
+        i0 = i1;
+        b1 = -INFINITY;
+        --known;
+      }
+      if (__any_sync(0xFFFFFFFFu, known == 0)) look();
       ++count;
       return true;
     };
@@ -342,10 +365,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : 
       inputs();
     }
     if (p.topk == 32) {  // no lane for the first one left out
-      float best = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) best = fmaxf(best, q[i]);
-      best = route_unkey(__reduce_max_sync(0xFFFFFFFFu, route_key(best)));
+      const float best = route_unkey(__reduce_max_sync(0xFFFFFFFFu, route_key(b0)));
       const float edge = __shfl_sync(0xFFFFFFFFu, mine, 31);
       again |= best != -INFINITY && edge != kMasked32 && !(edge - best > rel * 2.f + 0x1p-22f * (fabsf(edge) + fabsf(best)));
     }
@@ -354,8 +374,26 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : 
       route_exact<DT>(p, m, own);
       continue;
     }
-    // The scores of the taken in 64 bits.
     const bool has = lane < p.topk;
+    lk = route_clean(lk);
+    if (unsure == 0) {  // the order stands: 32 bits do for the weights, unless nearly nothing is to be divided by itself
+      float w = 0.f;
+      if (has && lk != -INFINITY) w = softmax ? expf(lk - top) : 1.f / (1.f + expf(-lk));
+      float of = softmax ? total : 1.f;
+      if (p.renorm) {
+        of = w;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) of += __shfl_xor_sync(0xFFFFFFFFu, of, d);
+      }
+      if (!p.renorm || of > 0x1p-20f) {
+        if (has) {
+          p.ids[(size_t)m * p.topk + lane] = id;
+          p.weights[(size_t)m * p.topk + lane] = (of > 0.f ? w / of : 0.f) * p.scale;
+        }
+        continue;
+      }
+    }
+    // The scores of the taken in 64 bits.
     double sum = 1.0, w = 0.0;
     if (softmax && (!p.renorm || unsure)) {
       sum = 0.0;
@@ -364,7 +402,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : 
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     }
-    lk = route_clean(lk);
     if (lane < count) w = route_score(p, lk, top, sum);
     if (unsure) {  // in their true order
       const double x = lane >= count ? -INFINITY : mine == kMasked32 ? kMaskedChoice : w + (double)bk;
