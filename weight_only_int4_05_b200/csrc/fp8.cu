@@ -1,6 +1,8 @@
 // fp8.cu -- fp8_quantize: a 16-bit matrix to e4m3 codes with one power-of-two scale per row and 128 columns.
 //
-// Bound by memory: 2 bytes read and 1 + 1/128 written per value.
+// Bound by memory: 2 bytes read and 1 + 1/128 written per value.  14336 x 4096 takes 28.7 us, 6.1 TB/s, 94 % of the measured
+// copy rate.  Measured on the way: the item number split by a 64-bit division, 43 us (the division took longer than the
+// quantizing); 32-bit steps with the next item's loads ahead, 28.7 us.
 #include "fp8.cuh"
 
 namespace awq {

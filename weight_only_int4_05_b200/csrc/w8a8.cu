@@ -12,6 +12,13 @@
 //               from shared to tensor memory (tcgen05.cp).
 //   warps 2, 3  scales: one 32-bit word per row holds the scales of 4 k-blocks; they fill the slots in turn.
 //   warps 4..11 epilogue, two warpgroups taking 16 tokens in turn: tensor memory -> registers -> y, or h = silu(gate) up quantized again.
+// What bounds it and what each part measured (us, B200):
+//   2048 x 28672 x 8192: the tensor cores, then the 1000 W cap (the SM clock falls to 1.2 - 1.4 GHz): 345 - 445, 2.2 - 2.8
+//     PFLOP/s by the card; 718 with one CTA per tile and one accumulator, whose epilogue nothing covered.
+//   16 x 14336 x 4096: the weight's bytes, 17.3 (3.5 TB/s; 7 of the 17 are the way from x to the first product, the joining
+//     of the parts and the hand-over between kernels, during which only the next kernel's first ring is fetched).
+//   1 x 4096 x 4096: latency, 9.4; 26 when 32 CTAs each took the whole of K.
+//   gate|up and down of 64 experts (4096/1024), 2048 tokens top 6: 117 and 93, 4.6 and 5.1 TB/s of weights and rows.
 // Two accumulators alternate, so a tile's epilogue runs under the next tile's products; where two do not fit beside the
 // scales they share some columns, which the epilogue reads first.
 // Many tokens (CG = 2): two CTAs work on one tile of 256 weight rows; each holds its 128 rows, half of the tokens' codes and
@@ -38,15 +45,22 @@ constexpr int kTileW = 128;        // weight rows per accumulator and CTA
 constexpr int kBlkBytes = 128;     // bytes of K per k-block: one swizzle row, one scale block
 template <int CG>
 constexpr int kEpi = 2;  // epilogue warpgroups
-constexpr int kXqMost = 16;        // tokens up to which the epilogue warps quantize x: 8 warps of 2 rows
-constexpr int kPartLeast = 8;      // k-blocks per part of a split K: joining parts takes about as long as 8 of them
-constexpr int kHalfMost = 32;      // tokens per tile up to which a CTA takes half an SM's shared memory
+// Tokens up to which the epilogue warps quantize x: 8 warps of 2 rows.  16 x 14336 x 4096 takes 17.3 us either way, but one
+// launch and no scratch instead of two and some (20 -> 13 us of host time); passes over up to 64 rows were slower than the
+// quantizer in front (333 x 1000 x 1040: 13.5 against 9.0 us).
+constexpr int kXqMost = 16;
+// k-blocks per part of a split K: joining parts takes about as long as 8 of them (1 x 4096 x 4096 in 4 parts of 8: 9.4 us, in
+// 8 parts of 4: 9.4; 9 k-blocks of an expert in 2 parts: 19 us, whole: 15.7).
+constexpr int kPartLeast = 8;
+// Tokens per tile up to which a CTA takes half an SM's shared memory: one token over two of eight 4096/14336 experts, 88 us
+// with whole SMs, 75 with halves.
+constexpr int kHalfMost = 32;
 template <int CG>
 constexpr int kW8Threads = 128 + 128 * kEpi<CG>;
 constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on sm_100
 constexpr int kW8HalfSmem = 115712;  // two blocks per SM (1 KB of each block's share is the system's)
-constexpr int kSplitMost = 64;     // tokens per tile up to which K is split
-constexpr int kPairLeast = 64;     // tokens per tile from which two CTAs work on it together
+constexpr int kSplitMost = 64;     // tokens per tile up to which K is split (64 x 4096 x 14336: 38 us whole, 20 split)
+constexpr int kPairLeast = 64;     // tokens per tile from which two CTAs work on it together (112: 151 us alone, 136 paired)
 constexpr int kSf = 4;             // scale slots (4 k-blocks each) in shared memory
 constexpr int kSfTmem = 2;         // and in tensor memory
 
@@ -166,6 +180,8 @@ __device__ __forceinline__ void w8_store(const W8Params& p, const W8Tile& t, int
     w8_store_as<W, __nv_bfloat16>(p, t, row, c, f, [](float v) { return __float2bfloat16_rn(v); });
 }
 
+// (Written straight from the registers the quantizing epilogue below took 24000 cycles per tile of 112 tokens, through shared
+// memory 14000, and gate|up of the experts 135 -> 118 us.)
 // The same through shared memory, for the pair's large tiles: 16 tokens of the 128 rows are turned round, so that a warp
 // writes whole runs of 128 outputs of 4 tokens (256 or 512 contiguous bytes) where it wrote 16 runs of 32; for outputs whose
 // row length is a multiple of 4.  `turned` is the warpgroup's [16][128]; v gets the 4 outputs of tokens 4 q .. 4 q + 3 from
