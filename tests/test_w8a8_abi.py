@@ -90,3 +90,24 @@ def test_python_refusals_on_the_host():
                  lambda: W.w8a8_moe(x, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2), m, m)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_calls_module_refuses_like_the_library(L):
+    """The CPython functions pass every argument on: the library's refusals come back, and arguments of another kind are
+    errors before the call."""
+    C, at = _lib.calls(), 0x10000
+    assert C.fp8_quantize(at, 3, 4, 512, at, at, None) == 2 and C.fp8_quantize(at, 1, 4, 504, at, at, 0) == 1
+    assert C.fp8_quantize(at, 1, 4, 512, at, at + 8, None) == 3
+    assert C.w8a8_gemm(at, at, at, at, at, 3, 4, 8, 512, None) == 2 and C.w8a8_gemm(at, None, at, at, at, 1, 4, 8, 512, None) == 1
+    assert C.w8a8_linear(at, 1, at, at, at, 400, 8192, 4096, None, 0, None) == 6
+    assert C.w8a8_linear(at, 1, at, at, at, 400, 8192, 4096, at, 16, None) == 6
+    assert C.moe_route(at, 3, None, 4, 64, 4, 3, 1, 1, 0, 1.0, at, at, None) == 2
+    assert C.moe_route(at, 3, None, 4, 64, 4, 1, 1, 1, 0, float("nan"), at, at, None) == 1
+    assert C.moe_route(at, 3, None, 4, 64, 4, 1, 1, 1, 0, 1, at, at + 8, None) == 3
+    assert C.w8a8_moe(at, 3, at, at, at, at, at, at, at, 4, 8, 2, 512, 256, 512, at, 1 << 40, None) == 2
+    assert C.w8a8_moe(at, 1, at, at, at, at, at, at, at, 4, 8, 2, 512, 250, 512, at, 1 << 40, None) == 1
+    assert C.w8a8_moe(at, 1, at, at, at, at, at, at, at, 4, 8, 2, 512, 256, 512, at, 100, None) == 6
+    for bad in ((at, 1, 4, 512, at, at), (at, 1, 1 << 40, 512, at, at, None), (at, 1, "4", 512, at, at, None),
+                (at, 1, 4.5, 512, at, at, None), ("x", 1, 4, 512, at, at, None)):
+        with pytest.raises((TypeError, OverflowError)):
+            C.fp8_quantize(*bad)

@@ -114,6 +114,21 @@ def load() -> ctypes.CDLL:
         return lib
 
 
+_calls = None
+
+
+def calls():
+    """The CPython module of the 8-bit operators' entry points (csrc/calls.c), over the same library."""
+    global _calls
+    if _calls is None:
+        load()
+        if not os.path.exists(_build.CALLS_PATH):
+            raise RuntimeError(f"{_build.CALLS_PATH} is missing: build it with `python -m weight_only_int4_05_b200.build`")
+        from . import _calls as module
+        _calls = module
+    return _calls
+
+
 def check(status: int, where: str) -> None:
     if status != 0:
         raise AwqError(where, status)

@@ -2,7 +2,8 @@
 
     python -m weight_only_int4_05_b200.build [--verbose]
 
-The library links the CUDA runtime statically, so it needs only the NVIDIA driver at run time.
+The library links the CUDA runtime statically, so it needs only the NVIDIA driver at run time.  The CPython module _calls
+(csrc/calls.c) is built beside it and linked against it.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -18,6 +20,8 @@ LIB_NAME = "libawq_w4a16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.cu", "prep.cu", "pack.cu", "gemv.cu", "gemm.cu", "noalloc.cu", "selftest.cu", "search.cu", "gptq.cu",
            "fp8.cu", "w8a8.cu", "route.cu", "moe.cu"]
+CALLS_SOURCE = "calls.c"
+CALLS_PATH = os.path.join(PKG_DIR, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 HEADERS = ["common.cuh", "internal.h", "fp8.cuh", "w8a8.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -30,15 +34,15 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [CALLS_SOURCE]]
     files.append(os.path.join(ROOT, "include", "awq_w4a16.h"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -57,7 +61,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         sys.stderr.write(res.stdout + res.stderr)
     os.replace(tmp, LIB_PATH)
+    _build_calls()
     return LIB_PATH
+
+
+def _build_calls() -> None:
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler found")
+    tmp = CALLS_PATH + f".{os.getpid()}.tmp"
+    cmd = [cc, "-O2", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}",
+           f"-I{os.path.join(ROOT, 'include')}", "-o", tmp, os.path.join(CSRC, CALLS_SOURCE), f"-L{PKG_DIR}",
+           f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("building _calls failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, CALLS_PATH)
 
 
 if __name__ == "__main__":

@@ -107,8 +107,8 @@ def fp8_quantize(x: torch.Tensor, out: Optional[Fp8Matrix] = None) -> Fp8Matrix:
                         torch.empty(*shape[:-1], fp8_scale_cols(K), dtype=_E8M0, device=dev))
     elif _need_matrix(out, "out", len(shape), dev) != shape:
         raise ValueError(f"out has shape {tuple(out.codes.shape)}, expected {tuple(shape)}")
-    status = _lib.load().fp8_quantize(x.data_ptr(), _DTYPES[x.dtype], R, K, out[0].data_ptr(), out[1].data_ptr(),
-                                      _current_stream(dev.index))
+    status = _lib.calls().fp8_quantize(x.data_ptr(), _DTYPES[x.dtype], R, K, out[0].data_ptr(), out[1].data_ptr(),
+                                       _current_stream(dev.index))
     if status:
         _lib.check(status, "fp8_quantize")
     return out
@@ -144,7 +144,7 @@ def w8a8_linear(x: Union[torch.Tensor, Fp8Matrix], w: Fp8Matrix, out: Optional[t
     if wk != K:
         raise ValueError(f"x has K={K}, w has K={wk}")
     y = _output(out, M, N, dtype, dev)
-    lib = _lib.load()
+    lib = _lib.calls()
     if quantized:
         status = lib.w8a8_gemm(x.codes.data_ptr(), x.scales.data_ptr(), w[0].data_ptr(), w[1].data_ptr(), y.data_ptr(),
                                _DTYPES[dtype], M, N, K, _current_stream(dev.index))
@@ -180,8 +180,9 @@ def moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", bias: Opt
         raise AwqError("moe_route", 1)
     ids = torch.empty(M, topk, dtype=torch.int32, device=dev)
     weights = torch.empty(M, topk, dtype=torch.float32, device=dev)
-    status = _lib.load().moe_route(logits.data_ptr(), _DTYPES[logits.dtype], at, M, E, topk, kind, groups, topk_groups,
-                                   bool(renorm), scale, ids.data_ptr(), weights.data_ptr(), _current_stream(dev.index))
+    status = _lib.calls().moe_route(logits.data_ptr(), _DTYPES[logits.dtype], at, M, E, topk, kind, groups, topk_groups,
+                                    1 if renorm else 0, scale, ids.data_ptr(), weights.data_ptr(),
+                                    _current_stream(dev.index))
     if status:
         _lib.check(status, "moe_route")
     return Routing(ids, weights)
@@ -213,7 +214,7 @@ def w8a8_moe(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up:
         raise ValueError(f"gate_up {tuple(gate_up.codes.shape)} and down {tuple(down.codes.shape)} do not match x's K={K}")
     y = _output(out, M, N, x.dtype, dev)
     ws, at, size = _scratch("w8a8_moe", w8a8_moe_workspace_bytes(M, E, topk, K, I, N), workspace, dev)
-    status = _lib.load().w8a8_moe(x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(), weights.data_ptr(), gate_up[0].data_ptr(),
+    status = _lib.calls().w8a8_moe(x.data_ptr(), _DTYPES[x.dtype], ids.data_ptr(), weights.data_ptr(), gate_up[0].data_ptr(),
                                   gate_up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), y.data_ptr(), M, E, topk, K,
                                   I, N, at, size, _current_stream(dev.index))
     if status:
