@@ -61,7 +61,8 @@ constexpr int kW8Smem = 232448;    // opt-in dynamic shared memory per block on 
 constexpr int kW8HalfSmem = 115712;  // two blocks per SM (1 KB of each block's share is the system's)
 constexpr int kSplitMost = 64;     // tokens per tile up to which K is split (64 x 4096 x 14336: 38 us whole, 20 split)
 constexpr int kPairLeast = 64;     // tokens per tile from which two CTAs work on it together (112: 151 us alone, 136 paired)
-constexpr int kSf = 4;             // scale slots (4 k-blocks each) in shared memory
+template <bool XQ>
+constexpr int kSf = XQ ? 2 : 4;    // scale slots (4 k-blocks each) in shared memory
 constexpr int kSfTmem = 2;         // and in tensor memory
 
 struct W8Params {
@@ -293,20 +294,23 @@ __device__ __forceinline__ void w8_silu_quant(const W8Params& p, const W8Tile& t
   }
 }
 
-// One tile's x into the ring (XQ): warp xw takes token rows 2 xw and 2 xw + 1, half a warp per row, 8 values per lane and
-// k-block.  Four k-blocks (one word of scales) go at a time, the loads of the next four behind them.
+// One tile's x into its own ring (XQ): warp xw takes token rows 2 xw and 2 xw + 1, half a warp per row, 8 values per lane and
+// k-block.  Four k-blocks go at a time, the loads of the next four behind them; their codes stand in slot cs of `xring`
+// beside the slot's scale words, so that one wait and one arrival serve all (with the codes in the weight's stages it
+// took five of each, 200 to 350 cycles apiece on the way from x to the first product: 1 x 4096 x 4096 9.4 us, now 8.7).
 struct XqState {
-  int s = 0, cs = 0;            // ring stage and scale slot
-  unsigned phase = 1, cphase = 1;
+  int cs = 0;  // scale slot
+  unsigned phase = 1;
 };
 template <int DT>
-__device__ __forceinline__ void w8_quantize_x(const W8Params& p, const W8Tile& t, uint8_t* xtile, uint8_t* sfx, int stage,
-                                              int slot, uint64_t* full, uint64_t* empty, uint64_t* sf_full,
-                                              uint64_t* sf_empty, volatile int* abort_flag, int kb0, int kb1, int xw,
-                                              int lane, XqState& st) {
+__device__ __forceinline__ void w8_quantize_x(const W8Params& p, const W8Tile& t, uint8_t* xring, uint8_t* sfx, int slot,
+                                              uint64_t* sf_full, uint64_t* sf_empty, volatile int* abort_flag, int kb0,
+                                              int kb1, int xw, int lane, XqState& st) {
   const int r = xw * 2 + (lane >> 4);
   const uint16_t* x = p.x + (size_t)(t.t0 + min(r, t.rows - 1)) * p.K + (lane & 15) * 8;
   const int last = r < t.rows ? p.K - (lane & 15) * 8 : 0;  // columns from here on exist (in steps of 8)
+  // 128-byte swizzle: 16-byte piece n of row r stands at piece n ^ (r % 8)
+  uint8_t* to = xring + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
   uint4 v[4];
   auto load = [&](int c) {
 #pragma unroll
@@ -341,36 +345,16 @@ __device__ __forceinline__ void w8_quantize_x(const W8Params& p, const W8Tile& t
       q[j].y = e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16);
     }
     if (c + 1 < c1) load(c + 1);
-    int s = st.s;
-    unsigned phase = st.phase;
+    if (!warp_wait(&sf_empty[st.cs], st.phase, p.status, abort_flag)) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (4 * c + j < kb0 || 4 * c + j >= kb1) continue;
-      if (!warp_wait(&empty[s], phase, p.status, abort_flag)) return;
-      // 128-byte swizzle: 16-byte piece n of row r stands at piece n ^ (r % 8)
-      *reinterpret_cast<uint2*>(xtile + s * stage + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8) = q[j];
-      if (++s == p.ST) {
-        s = 0;
-        phase ^= 1u;
-      }
-    }
-    if (!warp_wait(&sf_empty[st.cs], st.cphase, p.status, abort_flag)) return;
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint2*>(to + (st.cs * 4 + j) * (16 * kBlkBytes)) = q[j];
     if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(sfx + st.cs * slot + r * 16) = word;  // rows 0 .. 31: the first word of 16 bytes
     fence_proxy_async_smem();
     __syncwarp();
-    s = st.s;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (4 * c + j < kb0 || 4 * c + j >= kb1) continue;
-      if (lane == 0) mbar_arrive(&full[s]);
-      if (++s == p.ST) s = 0;
-    }
     if (lane == 0) mbar_arrive(&sf_full[st.cs]);
-    st.s = s;
-    st.phase = phase;
-    if (++st.cs == kSf) {
+    if (++st.cs == kSf<true>) {
       st.cs = 0;
-      st.cphase ^= 1u;
+      st.phase ^= 1u;
     }
   }
 }
@@ -382,15 +366,16 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
   constexpr int NA = kAtomsA<EPI>;
   extern __shared__ uint8_t w8_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w8_smem_raw) + 1023) & ~uintptr_t(1023));
-  const int stage = w8_stage(NA, p.BT / CG), slot = w8_sf_slot(NA, p.BT);
+  const int stage = w8_stage(NA, XQ ? 0 : p.BT / CG), slot = w8_sf_slot(NA, p.BT);
   uint8_t* sf = smem + p.ST * stage;
-  float* part = reinterpret_cast<float*>(sf + kSf * slot);  // splits > 1: [NA * BT][128] partial sums
+  uint8_t* xring = sf + kSf<XQ> * slot;  // XQ: the codes of x, 4 k-blocks of 16 rows per scale slot
+  float* part = reinterpret_cast<float*>(xring + (XQ ? kSf<XQ> * 4 * 16 * kBlkBytes : 0));  // splits > 1: [NA * BT][128] partial sums
   // a pair: [kEpi][16][128], the epilogue's turning space in its place
   uint64_t* full = reinterpret_cast<uint64_t*>(part + (CG == 2 ? kEpi<CG> * 16 * kTileW : p.splits > 1 ? NA * p.BT * kTileW : 0));
   uint64_t* empty = full + p.ST;
   uint64_t* sf_full = empty + p.ST;
-  uint64_t* sf_empty = sf_full + kSf;
-  uint64_t* acc_full = sf_empty + kSf;
+  uint64_t* sf_empty = sf_full + kSf<XQ>;
+  uint64_t* acc_full = sf_empty + kSf<XQ>;
   uint64_t* acc_free = acc_full + 2;  // one of each per accumulator: the products may run two tiles ahead of the epilogue
   uint64_t* drain = acc_free + 2;
   uint64_t* part_full = drain + 1;
@@ -406,10 +391,10 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
   const int csize = CG == 2 ? 2 : p.splits;  // CTAs that share a tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ST; ++s) {
-      mbar_init(&full[s], XQ ? 1 + 4 * kEpi<CG> : 1);
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < kSf; ++s) {
+    for (int s = 0; s < kSf<XQ>; ++s) {
       mbar_init(&sf_full[s], XQ ? 1 + 4 * kEpi<CG> : CG);
       mbar_init(&sf_empty[s], 1);
     }
@@ -464,7 +449,7 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
       // In a pair both CTAs' copies count on the even CTA's barrier, which expects the bytes of both.
       const uint32_t full0 = CG == 2 ? cluster_addr(full, 0) : smem_u32(full);
       auto load_w = [&](const W8Tile& t, int kb, int s) {
-        if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(XQ ? NA * kTileW * kBlkBytes : CG * stage));
+        if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[s], (unsigned)(CG * stage));
 #pragma unroll
         for (int a = 0; a < NA; ++a)
           tma_load_2d_group<CG>(base + s * stage + a * kTileW * kBlkBytes, &maps.w, kb * kBlkBytes, t.w0 + a * p.N,
@@ -525,7 +510,7 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
       unsigned phase = 0, cphase = 0;
       int filled = 0;                       // chunks so far, up to kSfTmem
       bool ok = true;
-      const uint32_t base = smem_u32(smem), sfbase = smem_u32(sf);
+      const uint32_t base = smem_u32(smem), sfbase = smem_u32(sf), xbase = smem_u32(xring);
       for (int tile = first_tile; tile < tiles && ok; tile += tile_step, ++done) {
         // The accumulator is free once the epilogue has read the tile that it held last, two tiles ago (a barrier for each);
         // where the two share columns, once it has read those of the tile before this one (the first barrier).
@@ -540,10 +525,12 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
           const uint32_t sfa = sf_tmem + (uint32_t)ct * sf_cols, sfb = sfa + NA * 4;
           if ((kb & 3) == 0 || kb == kb0) {  // the scales of the next 4 k-blocks
             if (!(ok = warp_wait(&sf_full[cs], cphase, p.status, abort_flag))) break;
-            if (filled < kSfTmem) {
+            if (kSf<XQ> <= kSfTmem) {
+              // a slot of each kind in step: whoever filled this one had waited for the same products
+            } else if (filled < kSfTmem) {
               ++filled;
             } else {  // the products that read this tensor-memory slot last are done (kSfTmem chunks ago)
-              const int was = (cs + kSf - kSfTmem) % kSf;
+              const int was = (cs + kSf<XQ> - kSfTmem) % kSf<XQ>;
               if (!(ok = warp_wait(&sf_empty[was], was > cs ? cphase ^ 1u : cphase, p.status, abort_flag))) break;
             }
             tc_fence_after_sync();
@@ -558,7 +545,8 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
           const bool last = (kb & 3) == 3 || kb == kb1 - 1;
           if (elect_one()) {
             const uint64_t wa = umma_desc_sw128(base + s * stage);
-            const uint64_t xb = umma_desc_sw128(base + s * stage + NA * kTileW * kBlkBytes);
+            const uint64_t xb = umma_desc_sw128(XQ ? xbase + (cs * 4 + (kb & 3)) * (16 * kBlkBytes)
+                                                   : base + s * stage + NA * kTileW * kBlkBytes);
             const uint32_t id = umma_idesc_sf(p.idesc, (uint32_t)(kb & 3));
             // descriptors count 16 bytes: + 2 per 32 channels, + 1024 per set of 128 rows
 #pragma unroll
@@ -578,7 +566,7 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
           }
           if (last) {
             ct = ct + 1 == kSfTmem ? 0 : ct + 1;
-            if (++cs == kSf) {
+            if (++cs == kSf<XQ>) {
               cs = 0;
               cphase ^= 1u;
             }
@@ -627,7 +615,7 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
           }
         }
         turn ^= 1;
-        if (++cs == kSf) {
+        if (++cs == kSf<XQ>) {
           cs = 0;
           phase ^= 1u;
         }
@@ -664,8 +652,8 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
       const W8Tile t = w8_tile<CG>(p, tabs, tile, rank);
       if constexpr (XQ) {
         auto quantize = [&](auto dt) {
-          w8_quantize_x<decltype(dt)::value>(p, t, smem + NA * kTileW * kBlkBytes, sf + NA * 512, stage, slot, full, empty,
-                                             sf_full, sf_empty, abort_flag, kb0, kb1, warp - 4, lane, xq);
+          w8_quantize_x<decltype(dt)::value>(p, t, xring, sf + NA * 512, slot, sf_full, sf_empty, abort_flag, kb0, kb1,
+                                             warp - 4, lane, xq);
         };
         if (p.xdt == AWQ_DTYPE_F16) quantize(std::integral_constant<int, AWQ_DTYPE_F16>{});
         else quantize(std::integral_constant<int, AWQ_DTYPE_BF16>{});
@@ -934,11 +922,14 @@ awq_status w8a8_launch(const W8Args& a) {
   // Few tokens: two CTAs per SM, so that the next kernel's weights are under way while this one ends.
   const bool half = cg == 1 && p.BT <= kHalfMost;
   const int slots = half ? 2 * sms : sms;
-  const int stage = w8_stage(atoms, p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
+  const bool xq = a.x != nullptr;
+  if (xq && (cg != 1 || a.groups || p.BT > kXqMost)) return AWQ_ERR_UNSUPPORTED;
+  const int stage = w8_stage(atoms, xq ? 0 : p.BT / cg), slot = w8_sf_slot(atoms, p.BT);
+  const int slots_sf = xq ? kSf<true> * (slot + 4 * 16 * kBlkBytes) : kSf<false> * slot;
   int rest;
   for (;; p.splits /= 2) {  // the parts of a split K and the tables of many groups may leave too little for the ring
     const int part = cg == 2 ? kEpi<2> * 16 * kTileW * 4 : p.splits > 1 ? atoms * p.BT * kTileW * 4 : 0;
-    rest = 1024 + kSf * slot + part + 512 + 64 + kEpi<1> * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
+    rest = 1024 + slots_sf + part + 512 + 64 + kEpi<1> * 512 + (a.groups ? (2 * a.groups + 2) * 4 : 0);
     p.ST = ((half ? kW8HalfSmem : kW8Smem) - rest) / stage;
     if (p.ST > 12) p.ST = 12;
     if (p.ST >= 2 || p.splits == 1) break;
@@ -951,9 +942,7 @@ awq_status w8a8_launch(const W8Args& a) {
   p.idesc = umma_idesc_mxf8(kTileW * cg, p.BT);
   W8Maps maps;
   if (!encode_codes(encode, &maps.w, a.wc, wtotal, a.K, kTileW)) return AWQ_ERR_CUDA;
-  const bool xq = a.x != nullptr;
   if (xq) {
-    if (cg != 1 || a.groups || p.BT > kXqMost || p.ST < 5) return AWQ_ERR_UNSUPPORTED;  // 4 k-blocks are quantized at a time
     p.x = a.x;
     p.K = a.K;
     p.xdt = a.xdt;
