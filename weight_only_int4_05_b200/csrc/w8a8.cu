@@ -15,16 +15,16 @@
 // What bounds it and what each part measured (us, B200):
 //   2048 x 28672 x 8192: the tensor cores, then the 1000 W cap (the SM clock falls to 1.2 - 1.4 GHz): 345 - 445, 2.2 - 2.8
 //     PFLOP/s by the card; 718 with one CTA per tile and one accumulator, whose epilogue nothing covered.
-//   16 x 14336 x 4096: the weight's bytes, 17.3 (3.5 TB/s; 7 of the 17 are the way from x to the first product, the joining
+//   16 x 14336 x 4096: the weight's bytes, 16.7 (3.6 TB/s; 6 of the 17 are the way from x to the first product, the joining
 //     of the parts and the hand-over between kernels, during which only the next kernel's first ring is fetched).
-//   1 x 4096 x 4096: latency, 9.4; 26 when 32 CTAs each took the whole of K.
+//   1 x 4096 x 4096: latency, 8.4; 26 when 32 CTAs each took the whole of K, 8.7 when the parts were fetched instead of sent.
 //   gate|up and down of 64 experts (4096/1024), 2048 tokens top 6: 117 and 93, 4.6 and 5.1 TB/s of weights and rows.
 // Two accumulators alternate, so a tile's epilogue runs under the next tile's products; where two do not fit beside the
 // scales they share some columns, which the epilogue reads first.
 // Many tokens (CG = 2): two CTAs work on one tile of 256 weight rows; each holds its 128 rows, half of the tokens' codes and
 // its half of the accumulator, so each byte of x brought to an SM serves 256 rows.
-// Few tokens (splits > 1): a cluster shares one tile, each CTA a part of K; the partial sums meet in shared memory
-// (each CTA finishes some of the tokens, summing the parts in rank order), so there is no workspace and no counter.
+// Few tokens (splits > 1): a cluster shares one tile, each CTA a part of K; each CTA finishes some of the tokens, whose parts
+// the others put into its shared memory and it sums in rank order, so there is no workspace and no counter.
 // At most 16 tokens (XQ): x comes as 16-bit values and the epilogue warps, idle until the tile's products are done,
 // quantize it into the ring, each CTA the part of K that it needs, so a decode step has no quantizer launch in front of it;
 // the codes and scales are those of fp8_quantize, bit for bit.
@@ -658,8 +658,8 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
         if (p.xdt == AWQ_DTYPE_F16) quantize(std::integral_constant<int, AWQ_DTYPE_F16>{});
         else quantize(std::integral_constant<int, AWQ_DTYPE_BF16>{});
       }
-      warp_wait(&acc_full[done & 1], (unsigned)(done >> 1) & 1u, p.status, abort_flag);
-      if (!all_ok()) break;
+      const bool there = warp_wait(&acc_full[done & 1], (unsigned)(done >> 1) & 1u, p.status, abort_flag);
+      if (EPI == kW8Store && CG == 1 ? !there : !all_ok()) break;  // one CTA's stores need no other warp
       tc_fence_after_sync();
       const int buf = done & 1;
       const uint32_t acc = tq + (buf ? (uint32_t)p.acc_off : 0u);
@@ -696,49 +696,51 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
         if (held) release();
         continue;
       }
-      // ---- split K: the parts of all CTAs of the cluster are summed in rank order, each CTA doing its share of the tokens
+      // ---- split K: each CTA finishes its share of the tokens.  Every CTA puts its parts straight into the shared memory of
+      // the CTA that finishes them, which sums them in rank order: part [rank][accumulator][token of the share][row].
+      const bool more = tile + tile_step < tiles;
+      const int share = p.BT / p.splits;                     // a multiple of 2
+      const uint32_t per_share = (65536u + share - 1) / share;  // t / share = t * per_share >> 16 for t < 64
       if (done > 0) warp_wait(part_free, (unsigned)((done - 1) & 1), p.status, abort_flag);
       for (int c = 16 * wg; c < NA * p.BT; c += 16 * kEpi<CG>) {
+        const int a = c >= p.BT ? 1 : 0, t0 = c - a * p.BT;  // the accumulator and its first token here
+        if (t0 >= t.rows) continue;
         uint32_t v[16];
         tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * kTileW + row] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j) {
+          if (t0 + j < t.rows) {
+            const uint32_t owner = (uint32_t)(t0 + j) * per_share >> 16;
+            const int place = (rank * NA + a) * share + (t0 + j - (int)owner * share);
+            st_cluster_f32(cluster_addr(part + place * kTileW + row, owner), __uint_as_float(v[j]));
+          }
+        }
       }
-      release();
+      __syncwarp();
       // one lane per CTA of the cluster: each arrival carries a release, and eight in a row would take microseconds
       if (lane < p.splits) mbar_arrive_cluster(cluster_addr(part_full, (uint32_t)lane));
-      warp_wait<true>(part_full, (unsigned)(done & 1), p.status, abort_flag);
-      if (!all_ok()) break;
-      const int share = p.BT / p.splits;  // tokens per CTA, a multiple of 2
-#pragma unroll 2
-      for (int c = rank * share + 2 * wg; c < min((rank + 1) * share, t.rows); c += 2 * kEpi<CG>) {
-        float v[8][2], u[8][2];  // all parts in flight at once
+      if (more) release();
+      bool joined = warp_wait<true>(part_full, (unsigned)(done & 1), p.status, abort_flag);
+      if (EPI == kW8SiluQuant && !(joined = all_ok())) break;  // its warps meet below, the others nowhere
+      const int end = joined ? min(share, t.rows - rank * share) : 0;
+      for (int c = 2 * wg; c < end; c += 2 * kEpi<CG>) {
+        float f[2] = {0.f, 0.f}, g[2] = {0.f, 0.f};
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          const uint32_t src = cluster_addr(part + c * kTileW + row, (uint32_t)min(r, p.splits - 1));
+          if (r < p.splits) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            v[r][j] = u[r][j] = 0.f;
-            if (r < p.splits) {
-              v[r][j] = ld_cluster_f32(src + j * kTileW * 4);
-              if (NA == 2) u[r][j] = ld_cluster_f32(src + (p.BT + j) * kTileW * 4);
+            for (int j = 0; j < 2; ++j) {
+              f[j] += part[(r * NA * share + c + j) * kTileW + row];
+              if (NA == 2) g[j] += part[((r * NA + 1) * share + c + j) * kTileW + row];
             }
           }
         }
-        float f[2] = {0.f, 0.f}, g[2] = {0.f, 0.f};
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            f[j] += v[r][j];
-            if (NA == 2) g[j] += u[r][j];
-          }
-        if constexpr (EPI == kW8Store) w8_store<2>(p, t, row, c, f);
-        else w8_silu_quant<2>(p, t, row, c, f, g, my_amax, turn, 2 + wg);
+        if constexpr (EPI == kW8Store) w8_store<2>(p, t, row, rank * share + c, f);
+        else w8_silu_quant<2>(p, t, row, rank * share + c, f, g, my_amax, turn, 2 + wg);
       }
       __syncwarp();
-      if (lane < p.splits) mbar_arrive_cluster(cluster_addr(part_free, (uint32_t)lane));
+      if (more && lane < p.splits) mbar_arrive_cluster(cluster_addr(part_free, (uint32_t)lane));
     }
   }
   tc_fence_before_sync();
