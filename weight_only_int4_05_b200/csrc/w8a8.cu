@@ -52,8 +52,8 @@ constexpr int kXqMost = 16;
 // k-blocks per part of a split K: joining parts takes about as long as 8 of them (1 x 4096 x 4096 in 4 parts of 8: 9.4 us, in
 // 8 parts of 4: 9.4; 9 k-blocks of an expert in 2 parts: 19 us, whole: 15.7).
 constexpr int kPartLeast = 8;
-// Tokens per tile up to which a CTA takes half an SM's shared memory: one token over two of eight 4096/14336 experts, 88 us
-// with whole SMs, 75 with halves.
+// Accumulator columns up to which a CTA takes half an SM's shared memory: one token over two of eight 4096/14336 experts, 88 us
+// with whole SMs, 75 with halves.  With 64 columns of gate|up (two weight tiles of 16 KB per stage) a half holds two stages only.
 constexpr int kHalfMost = 32;
 template <int CG>
 constexpr int kW8Threads = 128 + 128 * kEpi<CG>;
@@ -907,7 +907,7 @@ awq_status w8a8_launch(const W8Args& a) {
     shape = W8Shape{a.bt, a.bt >= kPairLeast ? 2 : 1, 1};
     const long long single = token_tiles(a.bt) * ((a.N + kTileW - 1) / kTileW);
     if (a.bt <= kSplitMost) {  // few tiles of a long K are split instead of paired
-      const int splits = split_k(single, p.KB, a.bt <= kHalfMost ? 2 * sms : sms);
+      const int splits = split_k(single, p.KB, a.bt * atoms <= kHalfMost ? 2 * sms : sms);
       if (shape.cg == 1 || splits > 1) shape = W8Shape{a.bt, 1, splits};
     }
   } else {
@@ -922,7 +922,7 @@ awq_status w8a8_launch(const W8Args& a) {
   const long long bound = token_tiles(p.BT) * p.n_tiles;
   if (bound > 0x7FFFFFFF || wtotal > 0x7FFFFFFF) return AWQ_ERR_UNSUPPORTED;
   // Few tokens: two CTAs per SM, so that the next kernel's weights are under way while this one ends.
-  const bool half = cg == 1 && p.BT <= kHalfMost;
+  const bool half = cg == 1 && p.BT * atoms <= kHalfMost;
   const int slots = half ? 2 * sms : sms;
   const bool xq = a.x != nullptr;
   if (xq && (cg != 1 || a.groups || p.BT > kXqMost)) return AWQ_ERR_UNSUPPORTED;
