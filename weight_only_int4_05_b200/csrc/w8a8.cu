@@ -11,7 +11,8 @@
 //   warp 1      MMA: per k-block 4 x tcgen05.mma (32 channels each); every 4th k-block first copies the next scale words
 //               from shared to tensor memory (tcgen05.cp).
 //   warps 2, 3  scales: one 32-bit word per row holds the scales of 4 k-blocks; they fill the slots in turn.
-//   warps 4..11 epilogue, two warpgroups taking 16 tokens in turn: tensor memory -> registers -> y, or h = silu(gate) up quantized again.
+//   warps 4..11 epilogue, two warpgroups taking 16 tokens (a lone CTA's: 4) in turn: tensor memory -> registers -> y, or
+//               h = silu(gate) up quantized again.
 // What bounds it and what each part measured (us, B200):
 //   2048 x 28672 x 8192: the tensor cores, then the 1000 W cap (the SM clock falls to 1.2 - 1.4 GHz): 345 - 445, 2.2 - 2.8
 //     PFLOP/s by the card; 718 with one CTA per tile and one accumulator, whose epilogue nothing covered.
@@ -45,12 +46,12 @@ constexpr int kTileW = 128;        // weight rows per accumulator and CTA
 constexpr int kBlkBytes = 128;     // bytes of K per k-block: one swizzle row, one scale block
 template <int CG>
 constexpr int kEpi = 2;  // epilogue warpgroups
-// Tokens up to which the epilogue warps quantize x: 8 warps of 2 rows.  16 x 14336 x 4096 takes 17.3 us either way, but one
-// launch and no scratch instead of two and some (20 -> 13 us of host time); passes over up to 64 rows were slower than the
-// quantizer in front (333 x 1000 x 1040: 13.5 against 9.0 us).
+// Tokens up to which the epilogue warps quantize x: 8 warps of 2 rows.  16 x 14336 x 4096 takes 16.7 us, 17.6 with the quantizer
+// in front, and a call one launch and no scratch instead of two and some (13 instead of 20 us on the host); passes over up to
+// 64 rows were slower than the quantizer in front (333 x 1000 x 1040: 13.5 against 9.0 us).
 constexpr int kXqMost = 16;
-// k-blocks per part of a split K: joining parts takes about as long as 8 of them (1 x 4096 x 4096 in 4 parts of 8: 9.4 us, in
-// 8 parts of 4: 9.4; 9 k-blocks of an expert in 2 parts: 19 us, whole: 15.7).
+// k-blocks per part of a split K: joining parts takes about as long as 8 of them (1 x 4096 x 4096 takes as long in 4 parts of 8
+// as in 8 parts of 4; 9 k-blocks of an expert's gate|up took 19 us in 2 parts and 15.7 whole).
 constexpr int kPartLeast = 8;
 // Accumulator columns up to which a CTA takes half an SM's shared memory: one token over two of eight 4096/14336 experts, 88 us
 // with whole SMs, 75 with halves.  With 64 columns of gate|up (two weight tiles of 16 KB per stage) a half holds two stages only.
@@ -515,8 +516,8 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
         // The accumulator is free once the epilogue has read the tile that it held last, two tiles ago (a barrier for each);
         // where the two share columns, once it has read those of the tile before this one (the first barrier).
         if (apart ? done > 1 : done > 0) {
-          const bool freed = apart ? warp_wait(&acc_free[done & 1], (unsigned)((done >> 1) - 1) & 1u, p.status, abort_flag)
-                                   : warp_wait(&acc_free[0], (unsigned)(done - 1) & 1u, p.status, abort_flag);
+          const bool freed = apart ? warp_wait<CG == 2>(&acc_free[done & 1], (unsigned)((done >> 1) - 1) & 1u, p.status, abort_flag)
+                                   : warp_wait<CG == 2>(&acc_free[0], (unsigned)(done - 1) & 1u, p.status, abort_flag);
           if (!freed) break;
         }
         tc_fence_after_sync();
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
         for (int kb = kb0; kb < kb1; ++kb) {
           const uint32_t sfa = sf_tmem + (uint32_t)ct * sf_cols, sfb = sfa + NA * 4;
           if ((kb & 3) == 0 || kb == kb0) {  // the scales of the next 4 k-blocks
-            if (!(ok = warp_wait(&sf_full[cs], cphase, p.status, abort_flag))) break;
+            if (!(ok = warp_wait<CG == 2>(&sf_full[cs], cphase, p.status, abort_flag))) break;
             if (kSf<XQ> <= kSfTmem) {
               // a slot of each kind in step: whoever filled this one had waited for the same products
             } else if (filled < kSfTmem) {
@@ -920,7 +921,7 @@ awq_status w8a8_launch(const W8Args& a) {
   p.n_tiles = (a.N + kTileW * cg - 1) / (kTileW * cg);
   p.t_tiles = (int)token_tiles(p.BT);
   const long long bound = token_tiles(p.BT) * p.n_tiles;
-  if (bound > 0x7FFFFFFF || wtotal > 0x7FFFFFFF) return AWQ_ERR_UNSUPPORTED;
+  if (bound > 0x7FFF0000 || wtotal > 0x7FFF0000) return AWQ_ERR_UNSUPPORTED;
   // Few tokens: two CTAs per SM, so that the next kernel's weights are under way while this one ends.
   const bool half = cg == 1 && p.BT * atoms <= kHalfMost;
   const int slots = half ? 2 * sms : sms;
