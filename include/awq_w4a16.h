@@ -391,6 +391,8 @@ size_t w4a16_workspace_bytes(int mode, int M, int N, int K, int g);
  * workspaces of these calls need no zero-fill and hold nothing from one call to the next.  A value that is NaN gives a NaN
  * code; an infinite one is undefined behaviour.  fp8_quantize never signals its dependents early, so it may be followed by
  * a product on the weights that it wrote, as awq_pack.
+ *   What a call writes must not overlap what it reads, nor its workspace (AWQ_ERR_INVALID_ARG); w8a8_moe alone may write y
+ * over x.
  */
 #define AWQ_DTYPE_F16 1
 #define AWQ_DTYPE_BF16 2

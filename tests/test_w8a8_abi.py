@@ -57,6 +57,35 @@ def test_linear_checks(L):
     assert mm(dt=3) == 2 and mm(M=0) == 1 and mm(K=8) == 1 and mm(xs=None) == 1 and mm(xs=ODD) == 3 and mm(xc=ODD) == 3
 
 
+def test_outputs_over_inputs_are_refused(L):
+    """Every call here has one pair of arrays that share bytes, its last 16 among them, and is refused before a launch."""
+    far = [(i + 1) << 40 for i in range(11)]
+    def refused(call, n, i, nbytes, j):  # array j starts in the last 16 bytes of array i
+        for at in (far[i], far[i] + nbytes - 16):
+            p = far[:n]
+            p[j] = at
+            assert call([P(v) for v in p]) == 1, (i, j)
+    q = lambda p: L.fp8_quantize(p[0], 1, 64, 512, p[1], p[2], None)  # noqa: E731
+    refused(q, 3, 0, 64 * 512 * 2, 1), refused(q, 3, 0, 64 * 512 * 2, 2), refused(q, 3, 1, 64 * 512, 2)
+    mm = lambda p: L.w8a8_gemm(p[0], p[1], p[2], p[3], p[4], 1, 64, 32, 512, None)  # noqa: E731
+    for i, n in ((0, 64 * 512), (1, 64 * 4), (2, 32 * 512), (3, 32 * 4)):
+        refused(mm, 5, i, n, 4)
+    for M in (4, 64):
+        lin = lambda p: L.w8a8_linear(p[0], 1, p[1], p[2], p[3], M, 32, 512, p[4], 1 << 40, None)  # noqa: E731
+        for i, n in ((0, M * 512 * 2), (1, 32 * 512), (2, 32 * 4)):
+            refused(lin, 5, i, n, 3)
+    refused(lin, 5, 0, 64 * 512 * 2, 4), refused(lin, 5, 3, 64 * 32 * 2, 4)
+    route = lambda p: L.moe_route(p[0], 3, p[1], 64, 64, 4, 1, 1, 1, 0, ctypes.c_float(1), p[2], p[3], None)  # noqa: E731
+    for i, n in ((0, 64 * 64 * 4), (1, 64 * 4)):
+        refused(route, 4, i, n, 2), refused(route, 4, i, n, 3)
+    refused(route, 4, 2, 64 * 4 * 4, 3)
+    moe = lambda p: L.w8a8_moe(p[0], 1, p[1], p[2], p[3], p[4], p[5], p[6], p[7], 64, 8, 2, 512, 256, 128, p[8],  # noqa: E731
+                               1 << 40, None)
+    refused(moe, 9, 2, 64 * 2 * 4, 7)
+    for i, n in ((0, 64 * 512 * 2), (1, 64 * 2 * 4), (2, 64 * 2 * 4), (7, 64 * 128 * 2)):
+        refused(moe, 9, i, n, 8)
+
+
 def test_route_checks(L):
     route = lambda l=F, dt=3, b=None, M=4, E=64, k=4, s=1, g=1, tg=1, sc=1.0, i=F, w=F: L.moe_route(  # noqa: E731
         l, dt, b, M, E, k, s, g, tg, 0, ctypes.c_float(sc), i, w, None)
@@ -101,6 +130,7 @@ def test_calls_module_refuses_like_the_library(L):
     assert C.w8a8_gemm(at, at, at, at, at, 3, 4, 8, 512, None) == 2 and C.w8a8_gemm(at, None, at, at, at, 1, 4, 8, 512, None) == 1
     assert C.w8a8_linear(at, 1, at, at, at, 400, 8192, 4096, None, 0, None) == 6
     assert C.w8a8_linear(at, 1, at, at, at, 400, 8192, 4096, at, 16, None) == 6
+    assert C.w8a8_linear(at, 1, at, at, at, 4, 512, 512, None, 0, None) == 1  # y over x
     assert C.moe_route(at, 3, None, 4, 64, 4, 3, 1, 1, 0, 1.0, at, at, None) == 2
     assert C.moe_route(at, 3, None, 4, 64, 4, 1, 1, 1, 0, float("nan"), at, at, None) == 1
     assert C.moe_route(at, 3, None, 4, 64, 4, 1, 1, 1, 0, 1, at, at + 8, None) == 3

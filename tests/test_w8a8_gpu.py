@@ -539,3 +539,24 @@ def test_two_streams_at_once():
             assert y.shape == want[(rep + 2 * i) % 4].shape and torch.isfinite(y).all()
             assert torch.equal(y, want[(rep + 2 * i) % 4])
     status_ok()
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_experts_in_place_and_other_overlaps_refused(M):
+    """w8a8_moe may write y over x; the other calls refuse an output over an input."""
+    rng = np.random.default_rng(34)
+    E, K, I = 8, 256, 144
+    gate, gu, gv, dn, dv = make_layer(rng, E, K, I, torch.bfloat16)
+    head, hv = matrix(rng, (K, K), 0.1)
+    x = activations(rng, M, K, torch.bfloat16).cuda()
+    ids, w = choose(rng, M, E, 2).cuda(), torch.rand(M, 2, device="cuda")
+    want = W.w8a8_moe(x, ids, w, gu, dn)
+    same = x.clone()
+    assert W.w8a8_moe(same, ids, w, gu, dn, out=same) is same
+    assert torch.equal(same, want)
+    with pytest.raises(W.AwqError):
+        W.w8a8_linear(x, head, out=x)
+    if M > 16:  # fewer tokens use no workspace
+        with pytest.raises(W.AwqError):
+            W.w8a8_linear(x, head, workspace=x.view(torch.uint8).view(-1))
+    status_ok()

@@ -354,6 +354,13 @@ awq_status awq_search_scale(const uint16_t* d_W, const uint16_t* d_xcal, int N, 
 static bool dtype16(int dt) { return dt == AWQ_DTYPE_F16 || dt == AWQ_DTYPE_BF16; }
 static bool size_ok(int v, int most, int multiple) { return v >= 1 && v <= most && v % multiple == 0; }
 
+// CTAs write while others still read, so an output over an input (or over another output) is refused.
+// Whether [a, a + na) and [b, b + nb) share a byte.
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 size_t fp8_scale_bytes(int R, int K) {
   if (!size_ok(R, 1 << 30, 1) || !size_ok(K, kMaxK, 16)) return SIZE_MAX;
   return (size_t)R * (size_t)fp8_scale_cols(K);
@@ -364,6 +371,9 @@ awq_status fp8_quantize(const void* d_x, int dtype, int R, int K, uint8_t* d_cod
   if (!dtype16(dtype)) return AWQ_ERR_UNSUPPORTED;
   if (!size_ok(R, 1 << 30, 1) || !size_ok(K, kMaxK, 16) || !d_x || !d_codes || !d_scales) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(d_x) || !aligned16(d_codes) || !aligned16(d_scales)) return AWQ_ERR_MISALIGNED;
+  const size_t nx = (size_t)R * K * 2, nc = (size_t)R * K, ns = fp8_scale_bytes(R, K);
+  if (overlap(d_codes, nc, d_x, nx) || overlap(d_scales, ns, d_x, nx) || overlap(d_codes, nc, d_scales, ns))
+    return AWQ_ERR_INVALID_ARG;
   return fp8_quantize_launch(d_x, dtype, R, K, d_codes, d_scales, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -401,6 +411,10 @@ awq_status w8a8_gemm(const uint8_t* d_xcodes, const uint8_t* d_xscales, const ui
   if (st != AWQ_OK) return st;
   if (!d_xscales) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(d_xscales)) return AWQ_ERR_MISALIGNED;
+  const size_t ny = (size_t)M * N * 2;
+  if (overlap(d_y, ny, d_xcodes, (size_t)M * K) || overlap(d_y, ny, d_xscales, fp8_scale_bytes(M, K)) ||
+      overlap(d_y, ny, d_wcodes, (size_t)N * K) || overlap(d_y, ny, d_wscales, fp8_scale_bytes(N, K)))
+    return AWQ_ERR_INVALID_ARG;
   return w8a8_product(d_xcodes, d_xscales, d_wcodes, d_wscales, d_y, dtype, M, N, K, stream);
 }
 
@@ -416,11 +430,17 @@ awq_status w8a8_linear(const void* d_x, int dtype, const uint8_t* d_wcodes, cons
                        int N, int K, void* d_workspace, size_t workspace_bytes, awq_stream_t stream) {
   awq_status st = check_w8a8(d_x, d_wcodes, d_wscales, d_y, dtype, M, N, K);
   if (st != AWQ_OK) return st;
+  const size_t nx = (size_t)M * K * 2, ny = (size_t)M * N * 2, need = w8a8_workspace_bytes(M, N, K);
+  if (need != 0 && (!d_workspace || workspace_bytes < need)) return AWQ_ERR_WORKSPACE;
+  if (need != 0 && !aligned16(d_workspace)) return AWQ_ERR_MISALIGNED;
+  if (overlap(d_y, ny, d_x, nx) || overlap(d_y, ny, d_wcodes, (size_t)N * K) ||
+      overlap(d_y, ny, d_wscales, fp8_scale_bytes(N, K)))
+    return AWQ_ERR_INVALID_ARG;
+  if (need != 0 && (overlap(d_workspace, need, d_x, nx) || overlap(d_workspace, need, d_y, ny)))
+    return AWQ_ERR_INVALID_ARG;
   if (w8a8_quantizes(M))
     return w8a8_product(nullptr, nullptr, d_wcodes, d_wscales, d_y, dtype, M, N, K, stream,
                         static_cast<const uint16_t*>(d_x));
-  if (!d_workspace || workspace_bytes < w8a8_workspace_bytes(M, N, K)) return AWQ_ERR_WORKSPACE;
-  if (!aligned16(d_workspace)) return AWQ_ERR_MISALIGNED;
   uint8_t* xc = static_cast<uint8_t*>(d_workspace);
   uint8_t* xs = xc + up256((size_t)M * K);
   st = fp8_quantize_launch(d_x, dtype, M, K, xc, xs, reinterpret_cast<cudaStream_t>(stream), true);
@@ -439,6 +459,11 @@ awq_status moe_route(const void* d_logits, int dtype, const float* d_bias, int M
   if (!(scale == scale) || !d_logits || !d_ids || !d_weights) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(d_logits) || (d_bias && !aligned16(d_bias)) || !aligned16(d_ids) || !aligned16(d_weights))
     return AWQ_ERR_MISALIGNED;
+  const size_t nl = (size_t)M * E * (dtype == AWQ_DTYPE_F32 ? 4 : 2), nb = d_bias ? (size_t)E * 4 : 0,
+               no = (size_t)M * topk * 4;
+  if (overlap(d_ids, no, d_logits, nl) || overlap(d_weights, no, d_logits, nl) || overlap(d_ids, no, d_weights, no) ||
+      (nb != 0 && (overlap(d_ids, no, d_bias, nb) || overlap(d_weights, no, d_bias, nb))))
+    return AWQ_ERR_INVALID_ARG;
   return moe_route_launch(d_logits, dtype, d_bias, M, E, topk, score, groups, topk_groups, renorm, scale, d_ids,
                           d_weights, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -467,6 +492,12 @@ awq_status w8a8_moe(const void* d_x, int dtype, const int32_t* d_ids, const floa
     return AWQ_ERR_MISALIGNED;
   if (!d_workspace || workspace_bytes < moe_workspace_bytes(M, E, topk, K, I, N)) return AWQ_ERR_WORKSPACE;
   if (!aligned16(d_workspace)) return AWQ_ERR_MISALIGNED;
+  // y may be x (only the last kernel writes it, when x has been read), but not the slots' weights, which that kernel reads.
+  const size_t need = moe_workspace_bytes(M, E, topk, K, I, N), ny = (size_t)M * N * 2, nr = (size_t)M * topk * 4;
+  if (overlap(d_y, ny, d_weights, nr) || overlap(d_workspace, need, d_y, ny) ||
+      overlap(d_workspace, need, d_x, (size_t)M * K * 2) || overlap(d_workspace, need, d_ids, nr) ||
+      overlap(d_workspace, need, d_weights, nr))
+    return AWQ_ERR_INVALID_ARG;
   MoeArgs a;
   a.x = static_cast<const uint16_t*>(d_x);
   a.ids = d_ids;
