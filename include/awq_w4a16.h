@@ -389,7 +389,7 @@ size_t w4a16_workspace_bytes(int mode, int M, int N, int K, int g);
  * K (and I) are multiples of 16; the last block of a row may be shorter than 128.  Rows and N are free.  The conventions of
  * the header hold (16-byte aligned pointers, row-major contiguous arrays, no allocation, no synchronisation), but the
  * workspaces of these calls need no zero-fill and hold nothing from one call to the next.  A value that is NaN gives a NaN
- * code; an infinite one is undefined behaviour.  fp8_quantize never signals its dependents early, so it may be followed by
+ * code and does not count in its block's scale; an infinite one counts as +-448 * 2^120.  fp8_quantize never signals its dependents early, so it may be followed by
  * a product on the weights that it wrote, as awq_pack.
  *   What a call writes must not overlap what it reads, nor its workspace (AWQ_ERR_INVALID_ARG); w8a8_moe alone may write y
  * over x.

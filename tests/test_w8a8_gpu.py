@@ -560,3 +560,26 @@ def test_experts_in_place_and_other_overlaps_refused(M):
         with pytest.raises(W.AwqError):
             W.w8a8_linear(x, head, workspace=x.view(torch.uint8).view(-1))
     status_ok()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M", [4, 40])
+def test_infinite_values_count_as_448_2_120(M, dtype):
+    """Code +-448 and scale byte 120 + 127, in the quantizer and in the product that quantizes by itself; the other
+    blocks and tokens keep theirs.  With weights of 2^-10 an infinite value alone gives 1.75 * 2^118: exact in bfloat16."""
+    rng = np.random.default_rng(35)
+    x = activations(rng, M, 256, TYPES[dtype])
+    clean = W.fp8_quantize(x.cuda())
+    x[1] = 0
+    x[1, 7], x[2, 130] = float("inf"), float("-inf")
+    q = W.fp8_quantize(x.cuda())
+    codes, scales = q.codes.float().cpu(), q.scales.view(torch.uint8).cpu()
+    assert codes[1, 7] == 448 and codes[2, 130] == -448 and scales[1, 0] == 247 and scales[2, 1] == 247
+    assert not torch.isnan(codes).any() and int((codes[1] != 0).sum()) == 1
+    assert torch.equal(q.codes[2, :128].view(torch.uint8), clean.codes[2, :128].view(torch.uint8))
+    w = W.fp8_quantize(torch.full((24, 256), 2.0 ** -10, dtype=torch.bfloat16, device="cuda"))
+    y, plain = W.w8a8_linear(x.cuda(), w), W.w8a8_linear(clean, w, dtype=TYPES[dtype])
+    assert torch.equal(y, W.w8a8_linear(q, w, dtype=TYPES[dtype]))
+    assert (y[1] == (1.75 * 2.0 ** 118 if dtype == "bf16" else float("inf"))).all()
+    assert torch.equal(y[0], plain[0]) and torch.equal(y[3:], plain[3:])
+    status_ok()
