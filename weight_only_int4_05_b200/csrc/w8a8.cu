@@ -19,7 +19,7 @@
 //   16 x 14336 x 4096: the weight's bytes, 16.7 (3.6 TB/s; 6 of the 17 are the way from x to the first product, the joining
 //     of the parts and the hand-over between kernels, during which only the next kernel's first ring is fetched).
 //   1 x 4096 x 4096: latency, 8.4; 26 when 32 CTAs each took the whole of K, 8.7 when the parts were fetched instead of sent.
-//   gate|up and down of 64 experts (4096/1024), 2048 tokens top 6: 117 and 93, 4.6 and 5.1 TB/s of weights and rows.
+//   gate|up and down of 64 experts (4096/1024), 2048 tokens top 6: 114 and 95 - 101, 5.3 and 4.8 - 5.1 TB/s of weights and rows.
 // Two accumulators alternate, so a tile's epilogue runs under the next tile's products; where two do not fit beside the
 // scales they share some columns, which the epilogue reads first.
 // Many tokens (CG = 2): two CTAs work on one tile of 256 weight rows; each holds its 128 rows, half of the tokens' codes and
@@ -182,12 +182,12 @@ __device__ __forceinline__ void w8_store(const W8Params& p, const W8Tile& t, int
     w8_store_as<W, __nv_bfloat16>(p, t, row, c, f, [](float v) { return __float2bfloat16_rn(v); });
 }
 
-// (Written straight from the registers the quantizing epilogue below took 24000 cycles per tile of 112 tokens, through shared
-// memory 14000, and gate|up of the experts 135 -> 118 us.)
 // The same through shared memory, for the pair's large tiles: 16 tokens of the 128 rows are turned round, so that a warp
 // writes whole runs of 128 outputs of 4 tokens (256 or 512 contiguous bytes) where it wrote 16 runs of 32; for outputs whose
 // row length is a multiple of 4.  `turned` is the warpgroup's [16][128]; v gets the 4 outputs of tokens 4 q .. 4 q + 3 from
-// output 4 lane on.
+// output 4 lane on.  Written straight from the registers the quantizing epilogue below took 24000 cycles per
+// tile of 112 tokens, this way 14000, and gate|up of the experts 118 us instead of 135.  A bulk copy per token from
+// shared memory in place of the wide stores was slower (the experts' down projection: 121 us against 95).
 __device__ __forceinline__ void w8_turn(const float (&f)[16], int row, uint32_t turned, int bar, float4 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i)
