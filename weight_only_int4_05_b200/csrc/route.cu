@@ -342,24 +342,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : 
     const float ln = __shfl_down_sync(0xFFFFFFFFu, lk, 1), bn = __shfl_down_sync(0xFFFFFFFFu, bk, 1);
     const float qn = __shfl_down_sync(0xFFFFFFFFu, mine, 1);
     // A sigmoid's error is below 2^-21 of it (the exponential 2^-22, the sum 2^-24, the quotient 2^-22).  A softmax's is
-    // below 2^-17: l - top rounds to 2^-24 of itself, which the exponential takes over (|l - top| < 104 where it is not 0),
+    // below 2^-16: l - top rounds to 2^-24 of itself, which the exponential takes over (|l - top| < 104 where it is not 0),
     // and the sum of up to 1024 terms to 37 * 2^-24.  A biased score rounds to 2^-24 of itself once more.
     const float rel = softmax ? 0x1p-16f : 0x1p-20f;
+    const float most = softmax ? inv : 1.f;  // no score of the row is larger
     bool order = false;  // the order of this one and the next is in doubt
     if (lane < count - 1 && lane < p.topk && mine != kMasked32) {
       // At the border a true tie is in doubt as well: an expert of another logit may stand behind it at the same 32-bit value.
-      const bool tie = lk == ln && bk == bn && lane != p.topk - 1;
-      const float err = rel * (fabsf(mine - bk) + fabsf(qn - bn)) + 0x1p-22f * (fabsf(mine) + fabsf(qn));
-      order = !tie && !(mine - qn > err);
+      const bool edge = lane == p.topk - 1, tie = lk == ln && bk == bn && !edge;
+      // Among the chosen two neighbours' errors are enough, since the doubt of any of them has all compared.  The last one in
+      // stands against all that are out: without a bias their scores, and so their errors, are smaller still; with one, a
+      // larger score that its bias lowers may stand anywhere behind, with an error of the largest score's.
+      const float of = edge && p.bias ? 2.f * most : fabsf(mine - bk) + fabsf(qn - bn);
+      order = !tie && !(mine - qn > rel * of + 0x1p-22f * (fabsf(mine) + fabsf(qn)));
     }
     const uint32_t unsure = __ballot_sync(0xFFFFFFFFu, order);
     bool again = __any_sync(0xFFFFFFFFu, doubt);
     if (unsure >> (p.topk - 1) & 1u) {
-      // The border itself: take on until the last one taken is clearly below it (a score is at most 1).
+      // The border itself: take on until the last one taken is clearly below it, and with it whatever stands behind.
       const float edge = __shfl_sync(0xFFFFFFFFu, mine, p.topk - 1);
       for (;;) {
         const float last = __shfl_sync(0xFFFFFFFFu, mine, count - 1);
-        if (edge - last > rel * 2.f + 0x1p-22f * (fabsf(edge) + fabsf(last))) break;
+        if (edge - last > rel * 2.f * most + 0x1p-22f * (fabsf(edge) + fabsf(last))) break;
         if (!(more = take())) {
           again |= count == 32;
           break;
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : 
     if (p.topk == 32) {  // no lane for the first one left out
       const float best = route_unkey(__reduce_max_sync(0xFFFFFFFFu, route_key(b0)));
       const float edge = __shfl_sync(0xFFFFFFFFu, mine, 31);
-      again |= best != -INFINITY && edge != kMasked32 && !(edge - best > rel * 2.f + 0x1p-22f * (fabsf(edge) + fabsf(best)));
+      again |= best != -INFINITY && edge != kMasked32 && !(edge - best > rel * 2.f * most + 0x1p-22f * (fabsf(edge) + fabsf(best)));
     }
     if (again) {
       __syncwarp();
