@@ -226,7 +226,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : 
       for (int d = 1; d < share; d <<= 1)
         route_top2(a, b, __shfl_xor_sync(0xFFFFFFFFu, a, d), __shfl_xor_sync(0xFFFFFFFFu, b, d));
       const float v = per > 1 ? a + b : a;
-      const float size = fabsf(a) + (per > 1 ? fabsf(b) : 0.f) + 2.f;  // bounds the sum and the two scores in it (0 .. 1)
+      // Bounds every group's sum and the two scores in it (0 .. 1).  The largest counts for all: a group whose large choices
+      // cancel may stand anywhere in the order with its error.
+      float size = group ? fabsf(a) + (per > 1 ? fabsf(b) : 0.f) + 2.f : 0.f;
+      size = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(size)));
       int before = 0;  // groups that come before this lane's
       bool near = false;
       for (int o = 0; o < p.groups; ++o) {
@@ -234,9 +237,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NE <= 4 ? 8 : NE <= 8 ? 5 : 
         before += (w > v || (w == v && o < g)) ? 1 : 0;
         near |= o != g && !(fabsf(w - v) > (softmax ? 0x1p-17f : 0x1p-20f) * size);
       }
-      // A doubtful neighbour matters where the border runs between the two: the last group in or the first one out.
-      doubt = group && near && p.topk_groups < p.groups &&
-              (before == p.topk_groups - 1 || before == p.topk_groups || !(size < 1e30f));
+      // The border is in doubt where the last group in or the first one out has a neighbour within the error: where the two are
+      // further apart than that, no group changes sides.
+      doubt = group && near && p.topk_groups < p.groups && (before == p.topk_groups - 1 || before == p.topk_groups);
       if (__any_sync(0xFFFFFFFFu, doubt) && !softmax) {
         // The groups' sums in 64 bits, where each group's two largest are clear of its third (or the whole token again).
         float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY;
