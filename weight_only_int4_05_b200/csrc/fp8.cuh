@@ -35,6 +35,20 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+// silu(a) = a / (1 + e^-a) to 2^-20 of it (2^-119 where it is smaller than that), for every a: its limits a and 0 at the ends,
+// NaN for NaN.  e^-a = 2^(hi + lo), -a log2(e) carried in two parts (the argument reduction of Cody and Waite, "Software Manual
+// for the Elementary Functions", 1980, with base 2), since hi alone is off by up to 126 * 2^-24.
+// Past |hi| = 126 lo does not count: below it e is 0, or lost beside 1; above it silu is 0 to 2^-119.  There lo may be infinite or
+// NaN (hi overflows from |a| = 2.36e38 on, and a itself may be infinite), and so may e.
+__device__ __forceinline__ float fp8_silu(float a) {
+  const float hi = -a * 1.44269504f;
+  const float lo = fmaf(-a, 1.44269504f, -hi) - a * 1.92596299e-8f;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi));
+  if (fabsf(hi) < 126.f) e = fmaf(e, lo * 0.693147181f, e);
+  return __fdividef(hi >= 126.f ? 0.f : a, 1.0f + e);
+}
+
 // ---------------------------------------------------------------- 16-bit types
 template <int DT>
 __device__ __forceinline__ float2 pair_to_f32(uint32_t v) {

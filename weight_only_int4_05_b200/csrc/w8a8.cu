@@ -127,17 +127,6 @@ struct W8Maps {
   CUtensorMap w, x;
 };
 
-// a / (1 + e^-a) to a few units of 2^-23: e^-a = 2^(hi + lo) with hi + lo = -a log2(e) carried in two parts, and the fast
-// quotient (a denominator past 2^126 gives 0; a / it is below 2^-119 there).
-__device__ __forceinline__ float w8_silu(float a) {
-  const float hi = -a * 1.44269504f;
-  const float lo = fmaf(-a, 1.44269504f, -hi) - a * 1.92596299e-8f;
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi));
-  e = hi < 126.f ? fmaf(e, lo * 0.693147181f, e) : e;  // past it e may be infinite, and inf * 0 is not a number
-  return __fdividef(a, 1.0f + e);
-}
-
 // W columns of this warp's 32 lanes of tensor memory; the registers hold them after tmem_wait_ld alone.
 template <int W>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[W]) {
@@ -240,7 +229,7 @@ __device__ __forceinline__ void w8_silu_quant_turned(const W8Params& p, const W8
   const int lane = row & 31, n = t.n0 + lane * 4, first = c + (row >> 5) * 4, rows = t.rows - first;
   float h[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) h[i] = w8_silu(a[i]) * b[i];
+  for (int i = 0; i < 16; ++i) h[i] = fp8_silu(a[i]) * b[i];
   if (t.n0 + row >= p.N) {  // rows of another expert or of none
 #pragma unroll
     for (int i = 0; i < 16; ++i) h[i] = 0.f;
@@ -277,7 +266,7 @@ __device__ __forceinline__ void w8_silu_quant(const W8Params& p, const W8Tile& t
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    h[i] = n < p.N ? w8_silu(a[i]) * b[i] : 0.f;
+    h[i] = n < p.N ? fp8_silu(a[i]) * b[i] : 0.f;
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h[i])));
     if (lane == i) mine = m;
   }
