@@ -354,7 +354,8 @@ awq_status awq_search_scale(const uint16_t* d_W, const uint16_t* d_xcal, int N, 
 static bool dtype16(int dt) { return dt == AWQ_DTYPE_F16 || dt == AWQ_DTYPE_BF16; }
 static bool size_ok(int v, int most, int multiple) { return v >= 1 && v <= most && v % multiple == 0; }
 
-// CTAs write while others still read, so an output over an input (or over another output) is refused.
+// CTAs write while others still read, and a workspace is written before the last read: an output or a workspace over anything
+// else that the call takes is refused.
 // Whether [a, a + na) and [b, b + nb) share a byte.
 static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -436,7 +437,9 @@ awq_status w8a8_linear(const void* d_x, int dtype, const uint8_t* d_wcodes, cons
   if (overlap(d_y, ny, d_x, nx) || overlap(d_y, ny, d_wcodes, (size_t)N * K) ||
       overlap(d_y, ny, d_wscales, fp8_scale_bytes(N, K)))
     return AWQ_ERR_INVALID_ARG;
-  if (need != 0 && (overlap(d_workspace, need, d_x, nx) || overlap(d_workspace, need, d_y, ny)))
+  if (need != 0 && (overlap(d_workspace, need, d_x, nx) || overlap(d_workspace, need, d_y, ny) ||
+                    overlap(d_workspace, need, d_wcodes, (size_t)N * K) ||
+                    overlap(d_workspace, need, d_wscales, fp8_scale_bytes(N, K))))
     return AWQ_ERR_INVALID_ARG;
   if (w8a8_quantizes(M))
     return w8a8_product(nullptr, nullptr, d_wcodes, d_wscales, d_y, dtype, M, N, K, stream,
@@ -492,12 +495,17 @@ awq_status w8a8_moe(const void* d_x, int dtype, const int32_t* d_ids, const floa
     return AWQ_ERR_MISALIGNED;
   if (!d_workspace || workspace_bytes < moe_workspace_bytes(M, E, topk, K, I, N)) return AWQ_ERR_WORKSPACE;
   if (!aligned16(d_workspace)) return AWQ_ERR_MISALIGNED;
-  // y may be x (only the last kernel writes it, when x has been read), but not the slots' weights, which that kernel reads.
-  const size_t need = moe_workspace_bytes(M, E, topk, K, I, N), ny = (size_t)M * N * 2, nr = (size_t)M * topk * 4;
-  if (overlap(d_y, ny, d_weights, nr) || overlap(d_workspace, need, d_y, ny) ||
-      overlap(d_workspace, need, d_x, (size_t)M * K * 2) || overlap(d_workspace, need, d_ids, nr) ||
-      overlap(d_workspace, need, d_weights, nr))
-    return AWQ_ERR_INVALID_ARG;
+  // y may be x: only the last kernel writes y, when x has been read.
+  const size_t need = moe_workspace_bytes(M, E, topk, K, I, N), ny = (size_t)M * N * 2;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } read[] = {{d_ids, (size_t)M * topk * 4},         {d_weights, (size_t)M * topk * 4},
+              {d_gu_codes, (size_t)E * 2 * I * K},   {d_gu_scales, fp8_scale_bytes(E * 2 * I, K)},
+              {d_down_codes, (size_t)E * N * I},     {d_down_scales, fp8_scale_bytes(E * N, I)}};
+  if (overlap(d_workspace, need, d_y, ny) || overlap(d_workspace, need, d_x, (size_t)M * K * 2)) return AWQ_ERR_INVALID_ARG;
+  for (const auto& r : read)
+    if (overlap(d_y, ny, r.at, r.bytes) || overlap(d_workspace, need, r.at, r.bytes)) return AWQ_ERR_INVALID_ARG;
   MoeArgs a;
   a.x = static_cast<const uint16_t*>(d_x);
   a.ids = d_ids;
