@@ -18,4 +18,5 @@ def load():
     assert res.returncode == 0, res.stdout + res.stderr
     lib = ctypes.CDLL(out)
     lib.silu_of.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]
+    lib.signal_then_run.argtypes = [ctypes.c_ulonglong, ctypes.c_void_p]
     return lib

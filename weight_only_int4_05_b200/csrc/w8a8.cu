@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
     }
   } else if (warp < 4) {
     const int which = warp - 2;
+    bool ahead = XQ;  // XQ: this warp's first slot is free; for the next ones the products have to run, and they wait for x
     int turn = 0, cs = 0;
     unsigned phase = 1;
     bool ok = true;
@@ -584,7 +585,10 @@ __global__ void __launch_bounds__(kW8Threads<CG>, CG == 1 ? 2 : 1) w8a8_kernel(c
               const int row = min(t.w0 + a * p.N + j * 32 + lane, p.wtotal - 1);
               va[a][j] = __ldg(p.ws + (size_t)row * p.SW + c);
             }
-          if (!XQ) pdl_wait_prior_grids();  // x's scales come from the kernel before this one, the weight's do not
+          // x's scales come from the kernel before this one, the weight's do not.  XQ: the bounded wait below starts behind that
+          // kernel as well, or it would count its time.
+          if (!ahead) pdl_wait_prior_grids();
+          ahead = false;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             vb[j] = 0;
