@@ -2,7 +2,7 @@
  * calls.c -- the 8-bit operators' entry points as CPython functions (module _calls).
  *
  * Argument marshalling alone, for calls whose kernels take a few microseconds: a foreign-function call with 7 to 17 arguments
- * costs 0.8 to 1.7 us, this one 0.1.  Each function takes the C arguments in order (addresses as whole numbers, None for
+ * costs 0.8 to 1.7 us, this one 0.17 (0.06 of it for the lock).  Each function takes the C arguments in order (addresses as whole numbers, None for
  * NULL) and returns the status code.  Linked against libawq_w4a16.so beside it; no torch type appears.
  */
 #define PY_SSIZE_T_CLEAN
@@ -27,11 +27,16 @@ static int count_ok(Py_ssize_t n, Py_ssize_t want) {
 
 #define P(i) as_ptr(a[i])
 #define I(i) as_int(a[i])
-/* The arguments are converted before the call and an error among them refuses it. */
-#define CALL(expr)                    \
-  do {                                \
+/* The arguments are converted before the call and an error among them refuses it.  The call itself runs without the
+ * interpreter's lock: a launch may wait for room in the stream's queue, and a host function in that stream for the lock. */
+#define CALL(expr)                     \
+  do {                                 \
+    long status;                       \
     if (PyErr_Occurred()) return NULL; \
-    return PyLong_FromLong((long)(expr)); \
+    Py_BEGIN_ALLOW_THREADS             \
+    status = (long)(expr);             \
+    Py_END_ALLOW_THREADS               \
+    return PyLong_FromLong(status);    \
   } while (0)
 
 static PyObject* py_fp8_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
