@@ -1,10 +1,12 @@
 """ctypes loader for libawq_w4a16.so (the C ABI of include/awq_w4a16.h).
 
-Loading fails loudly when the shared library has not been built: there is no fallback path.
+Loading fails loudly when the shared library has not been built: there is no fallback path.  (The CPython module of the 8-bit
+operators' calls has one, by ctypes into the same library.)
 """
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -117,15 +119,43 @@ def load() -> ctypes.CDLL:
 _calls = None
 
 
+def _foreign(fn):
+    """A ctypes function that refuses what csrc/calls.c refuses (ctypes alone cuts whole numbers to their type)."""
+    kinds = fn.argtypes
+
+    def call(*args):
+        if len(args) != len(kinds):
+            raise TypeError(f"{len(kinds)} arguments expected, {len(args)} given")
+        values = []
+        for a, kind in zip(args, kinds):
+            if kind is ctypes.c_float:
+                a = float(a) if hasattr(a, "__float__") else operator.index(a)
+            elif a is not None or kind is not ctypes.c_void_p:
+                a = operator.index(a)
+                if kind(a).value != (a or (None if kind is ctypes.c_void_p else 0)):
+                    raise OverflowError(f"{a} does not fit its type")
+            values.append(a)
+        return fn(*values)
+    return call
+
+
+class _ForeignCalls:
+    def __init__(self, lib: ctypes.CDLL):
+        for name in ("fp8_quantize", "w8a8_gemm", "w8a8_linear", "moe_route", "w8a8_moe"):
+            setattr(self, name, _foreign(getattr(lib, name)))
+
+
 def calls():
-    """The CPython module of the 8-bit operators' entry points (csrc/calls.c), over the same library."""
+    """The 8-bit operators' entry points: the CPython module (csrc/calls.c) over the same library, or, where it could not be
+    built, the library's functions by ctypes, about 1 us slower per call."""
     global _calls
     if _calls is None:
-        load()
-        if not os.path.exists(_build.CALLS_PATH):
-            raise RuntimeError(f"{_build.CALLS_PATH} is missing: build it with `python -m weight_only_int4_05_b200.build`")
-        from . import _calls as module
-        _calls = module
+        lib = load()
+        if os.path.exists(_build.CALLS_PATH):
+            from . import _calls as module
+            _calls = module
+        else:
+            _calls = _ForeignCalls(lib)
     return _calls
 
 
