@@ -441,7 +441,9 @@ size_t w8a8_workspace_bytes(int M, int N, int K);
  *   their sum if renorm != 0, times scale.  Equal values go by the lowest index.  A logit of -inf or NaN masks its expert: p = 0, and
  *   it comes after every unmasked one of the groups that stay; +inf counts as the largest fp32.  A bias below
  *   -1e30 (or NaN) masks its expert in the choice alone.  With nothing left
- *   (every chosen p is 0) the weights are 0.  The order is that of the 64-bit values; weights are computed in fp32.
+ *   (every chosen p is 0) the weights are 0.  The order is that of the 64-bit values.  The weights are computed in fp32: sigmoid
+ *   scores to 7 * 2^-24 of their value (19 * 2^-24 renormalised); softmax scores further off by about 2^-24 times how far their
+ *   logit is below the largest and per 32 experts; a score below 2^-126 may count as 0.
  *   d_logits [M][E] of dtype;  d_ids [M][topk] int32, d_weights [M][topk] fp32, written.
  *   1 <= E <= 1024, 1 <= topk <= min(32, E), groups divides E, groups <= 32, topk <= topk_groups * E / groups.
  * Errors: AWQ_ERR_UNSUPPORTED (dtype, score), AWQ_ERR_INVALID_ARG, AWQ_ERR_MISALIGNED, AWQ_ERR_CUDA.
