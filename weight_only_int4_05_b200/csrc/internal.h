@@ -86,7 +86,7 @@ awq_status search_launch(const uint16_t* W, const uint16_t* xcal, int N, int K, 
 // Expert router (route.cu): arguments validated by the caller.
 awq_status moe_route_launch(const void* logits, int dt, const float* bias, int M, int E, int topk, int score, int groups,
                             int topk_groups, int renorm, float scale, int32_t* ids, float* weights, cudaStream_t st);
-// Expert MLP (moe.cu): workspace bytes (0: too large) and the launch sequence (arguments validated by the caller).
+// Expert MLP (moe.cu): workspace bytes and the launch sequence (sizes and arguments validated by the caller).
 struct MoeArgs {
   const uint16_t* x = nullptr;
   const int32_t* ids = nullptr;

@@ -8,7 +8,7 @@
 // each copy within its expert, by chunks of 1024), place_kernel (the tables of the grouped product) and scatter_kernel (quantizes
 // into the sorted order); then 2 x w8a8_kernel and combine_kernel.
 // Measured (B200): one token, top 2 of 8 experts 4096/14336: 70 us, 5.1 TB/s of the two experts' bytes (54 us at the copy rate).
-// 2048 tokens, top 6 of 64 experts 4096/1024: 283 - 325 us; alone the kernels take rank 5, place 6, scatter 13.5, gate|up 114,
+// 2048 tokens, top 6 of 64 experts 4096/1024: 283 - 336 us; alone the kernels take rank 5, place 6, scatter 13.5, gate|up 114,
 // down 95 - 101, combine 33, the products at 82 and 73 % of the copy rate: the 32-bit rows of the down projection (201 MB each way)
 // cost about 60 of them, which rounding the rows to 16 bits would halve at 1.4 times the output's rounding error.
 #include "fp8.cuh"

@@ -6,10 +6,12 @@
 // The order is that of the 64-bit values: next to a border 32-bit scores would order experts by their rounding.  A warp
 // works in 32 bits and looks at the gaps that its choice rests on.  Where each is wider than the scores' error (or the two
 // experts have the same logit and bias, a true tie), the 64-bit order is the same; where one is not, the few experts in
-// question are compared in 64 bits; where a border between groups is in doubt, the warp does the token again in 64 bits.
+// question are compared in 64 bits; where a border between groups is in doubt, the group sums are, or the warp does the token again
+// in 64 bits.  Between the chosen the errors of two neighbours count.  What is left out is held against the largest error in the
+// row: with a bias an expert far behind may have a large score, and a group two large choices that cancel.
 // The weights are 32-bit values of the chosen experts' scores.
-// Bound by latency for few tokens (one token among 256 experts: 4.7 us) and by issue slots for many (8192 tokens: 19 us, about
-// 1600 instructions per token at 64 % of the issue rate; its 8.9 MB would take 1.4).  All in 64 bits it took 34 us; a
+// Bound by latency for few tokens (one token among 256 experts: 4.8 us) and by issue slots for many (8192 tokens: 19 us, 1615
+// instructions per token at 63 % of the issue rate; its 8.9 MB would take 1.4).  All in 64 bits it took 34 us; a
 // token done again in 64 bits for one doubtful gap cost 8 us of tail per call, which the comparisons in place avoid.
 #include "fp8.cuh"
 
@@ -63,8 +65,8 @@ __device__ __noinline__ void route_exact(const RouteParams& p, long long m, doub
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
   double sum = 0.0;
   if (p.score == AWQ_SCORE_SOFTMAX) {
-  #pragma unroll 4
-  for (int e = lane; e < p.E; e += 32)
+#pragma unroll 4
+    for (int e = lane; e < p.E; e += 32)
       sum += route_score(p, route_clean(route_logit<DT>(p.logits, (size_t)m * p.E + e)), top, 1.0);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
@@ -95,8 +97,8 @@ __device__ __noinline__ void route_exact(const RouteParams& p, long long m, doub
       before += (o > v || (o == v && g < lane)) ? 1 : 0;
     }
     const uint32_t kept = __ballot_sync(0xFFFFFFFFu, lane < p.groups && before < p.topk_groups);
-  #pragma unroll 4
-  for (int e = lane; e < p.E; e += 32)
+#pragma unroll 4
+    for (int e = lane; e < p.E; e += 32)
       if (!((kept >> (e / per)) & 1u)) qs[e] = -INFINITY;
     __syncwarp();
   }
@@ -104,8 +106,8 @@ __device__ __noinline__ void route_exact(const RouteParams& p, long long m, doub
   for (int k = 0; k < p.topk; ++k) {
     double bq = -INFINITY;
     int be = 0x7FFFFFFF;
-  #pragma unroll 4
-  for (int e = lane; e < p.E; e += 32)
+#pragma unroll 4
+    for (int e = lane; e < p.E; e += 32)
       if (qs[e] > bq) {
         bq = qs[e];
         be = e;

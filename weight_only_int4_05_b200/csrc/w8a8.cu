@@ -14,10 +14,12 @@
 //   warps 4..11 epilogue, two warpgroups taking 16 tokens (a lone CTA's: 4) in turn: tensor memory -> registers -> y, or
 //               h = silu(gate) up quantized again.
 // What bounds it and what each part measured (us, B200):
-//   2048 x 28672 x 8192: the tensor cores, then the 1000 W cap (the SM clock falls to 1.2 - 1.4 GHz): 345 - 445, 2.2 - 2.8
-//     PFLOP/s by the card; 718 with one CTA per tile and one accumulator, whose epilogue nothing covered.
-//   16 x 14336 x 4096: the weight's bytes, 16.7 (3.6 TB/s; 6 of the 17 are the way from x to the first product, the joining
-//     of the parts and the hand-over between kernels, during which only the next kernel's first ring is fetched).
+//   2048 x 28672 x 8192: the tensor cores, then the 1000 W cap (the SM clock falls to 1.2 - 1.5 GHz): 360 - 445, 2.2 - 2.7
+//     PFLOP/s by the card, the tensor pipe active 79 % of all cycles; 718 with one CTA per tile and one accumulator, whose
+//     epilogue nothing covered.
+//   16 x 14336 x 4096: the weight's bytes, 16.7 (3.6 TB/s; they would take 9.2, the rest goes to the way from x to the first
+//     product, the joining of the parts and the hand-over between kernels, during which only the next kernel's first ring is
+//     fetched).
 //   1 x 4096 x 4096: latency, 8.4; 26 when 32 CTAs each took the whole of K, 8.7 when the parts were fetched instead of sent.
 //   gate|up and down of 64 experts (4096/1024), 2048 tokens top 6: 114 and 95 - 101, 5.3 and 4.8 - 5.1 TB/s of weights and rows.
 // Two accumulators alternate, so a tile's epilogue runs under the next tile's products; where two do not fit beside the
